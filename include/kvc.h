@@ -369,6 +369,104 @@ KVC_API kvc_status indexer_topk(const float* scores, int64_t ld, const int64_t* 
 /* The largest n_visible indexer_topk accepts (its candidates stay on chip). */
 KVC_API int64_t kvc_topk_max_candidates(void);
 
+/* ---------------------------------------------------------------- rotary positions
+ * Partial RoPE of queries ([HCA] §4 (2): the last r dimensions only), the counterpart of
+ * the rotation the cache layout applies to its entries.  Because an entry is key and value
+ * at once, the attention output's last r channels come out rotated by the entries'
+ * positions; rotating them back by the query's position (inverse = 1) leaves relative
+ * positions only. */
+
+typedef enum kvc_rope_layout {
+  KVC_ROPE_INTERLEAVED = 0, /* pair j = dimensions 2j, 2j+1 of the last r (the cache layout) */
+  KVC_ROPE_HALF = 1         /* pair j = dimensions j, j + r/2 of the last r */
+} kvc_rope_layout;
+
+/* x [T, H, c] -> out [T, H, c], both `dtype` (KVC_F32 or KVC_BF16): channels [0, c - r) are
+ * copied, pair j of the last r channels of token t becomes
+ *     magnitude * (a cos - b sin, a sin + b cos),  angle = +-pos[t] * inv_freq[j]
+ * with the minus sign for inverse = 1.  inverse = 1 is the transpose of inverse = 0, hence
+ * also its gradient with respect to x.
+ *   pos : [T] int64 device;  inv_freq : [r / 2] fp32 device;  magnitude : finite
+ *   c % 8 == 0, r % 8 == 0, 0 <= r <= c, H >= 1;  x and out 16-byte aligned
+ *   out == x works in place (only the last r channels are then touched); any other overlap
+ *   of x and out returns KVC_ERR_POINTER.
+ * The angle is formed and reduced modulo 2 pi in fp64, its sine and cosine and the rotation
+ * in fp32; bf16 results are rounded once. */
+KVC_API kvc_status partial_rope(const void* x, void* out, kvc_dtype dtype, int64_t T, int32_t H,
+                                int64_t c, int32_t r, const int64_t* pos, const float* inv_freq,
+                                int32_t layout, int32_t inverse, float magnitude,
+                                kvc_stream stream);
+
+/* Frequencies for inv_freq, scaled for contexts longer than the trained one by parts.
+ * Host function, no GPU work: out is HOST memory, r / 2 floats (copy it to the device once).
+ *   f_j = base^(-2j / r);  factor = 1 gives f_j itself, otherwise
+ *   out_j = f_j (1 - g_j) + (f_j / factor) g_j,  g_j = clamp((j - lo) / (hi - lo), 0, 1)
+ * where pair r ln(original_len / (2 pi beta)) / (2 ln base) turns beta times over the trained
+ * length original_len, lo is that pair for beta_fast rounded down (at least 0) and hi for
+ * beta_slow rounded up (at most r - 1; at least lo + 0.001): fast pairs keep their frequency, slow ones
+ * are interpolated by `factor`.  Computed in fp64, rounded once.
+ *   KVC_ERR_SHAPE: r < 8, r % 8 != 0, base <= 1, factor < 1, and with factor > 1
+ *   original_len <= 0, beta_slow <= 0 or beta_fast <= beta_slow; a value that is not finite */
+KVC_API kvc_status kvc_rope_frequencies(int32_t r, double base, double factor, double original_len,
+                                        double beta_fast, double beta_slow, float* out);
+
+/* ---------------------------------------------------------------- shared-KV attention
+ * The attention that reads the compressed cache ([CSA] §6 and [HCA] §3-4: shared-KV
+ * multi-query attention over the compressed entries, a local window beside them, an
+ * attention sink per head).  A cache row is one entry, key and value of every head at once:
+ *   K_s = [nope_s / fp8_scale ; rope_s]   (the cache layout above: [rows, c - r] E4M3 bytes
+ *                                          and [rows, r] bf16)
+ * r == c keeps the entries wholly in bf16 (nope unused, e.g. csa_compress's bf16 output),
+ * r == 0 wholly in FP8 (rope unused).  Query t attends the rows of two groups under one
+ * softmax, for each head h:
+ *   x_s = scale * (q[t, h] . K_s),  m = all rows s of both groups,
+ *   out[t, h] = sum_s exp(x_s) K_s / D,  lse[t, h] = ln D,
+ *   D = sum_s exp(x_s) (+ exp(sink[h]) if sink is given)
+ * Group 1, the cache: rows key_start[t] + e, where e runs over
+ *   shared_kv_attention       all entries 0 <= e < n_visible[t]  (HCA layers);
+ *   shared_kv_attention_topk  the list idx[t * k + j], j < min(k, n_visible[t]) (CSA layers;
+ *                             the output of indexer_topk as it stands): -1 lists nothing, an
+ *                             entry listed twice counts twice.
+ * Group 2, the window (optional: win_start == NULL leaves it out): rows win_start[t] .. +
+ *   win_len[t] - 1 of win_nope / win_rope, the same layout, r and fp8_scale; win_len[t] <=
+ *   max_win.  It may be the cache's own arrays.
+ * A query without a single row gets out = 0 and lse = sink[h] (-inf without a sink).
+ *   q [T, H, c] bf16 (its last r channels already rotated: partial_rope);  out [T, H, c]
+ *   bf16, not overlapping q;  lse [T, H] fp32 or NULL;  sink [H] fp32 or NULL (-inf: none)
+ *   key_start, n_visible, win_start, win_len [T] int64;  idx [T, k] int32
+ *   c % 8 == 0, r % 8 == 0, 0 <= r <= c and ceil((c - r) / 64) + ceil(r / 64) <= 8, else
+ *   KVC_ERR_UNSUPPORTED;  H >= 1;  1 <= k <= 2^20;  fp8_scale finite and > 0;  scale finite
+ *   q, nope, rope, out 16-byte aligned.
+ * Checked on the device: a query whose n_visible is negative or (dense) above max_visible,
+ *   whose win_len leaves [0, max_win], or one of whose groups leaves its arrays, is skipped
+ *   (out and lse rows untouched); a listed entry outside [-1, n_visible[t]) is left out of
+ *   the sums.  kvc_device_status() then reports KVC_ERR_INDEX.
+ * Arithmetic: E4M3 and bf16 operands are widened exactly; dot products, softmax statistics
+ *   and output sums are fp32; bf16 outputs are rounded once.
+ * workspace: device memory, 256-byte aligned, at least
+ *   shared_kv_attention_workspace_bytes(T, H, c, r, most) with most = max_visible (or k) +
+ *   max_win; it holds the partial sums of queries whose rows are split among the GPU's
+ *   processors.  Nothing in it outlives the call; calls whose work may overlap on the GPU
+ *   need one each (two captured graphs that may run at once included).  0 bytes: it is not
+ *   used and may be NULL.
+ *   The result does not depend on what else runs: each sum has a fixed order. */
+KVC_API int64_t shared_kv_attention_workspace_bytes(int64_t T, int32_t H, int64_t c, int32_t r,
+                                                    int64_t most_rows);
+KVC_API kvc_status shared_kv_attention(
+    const void* q, int64_t T, int32_t H, int64_t c, int32_t r, const void* nope, const void* rope,
+    int64_t cache_rows, float fp8_scale, const int64_t* key_start, const int64_t* n_visible,
+    int64_t max_visible, const void* win_nope, const void* win_rope, int64_t win_rows,
+    const int64_t* win_start, const int64_t* win_len, int64_t max_win, const float* sink,
+    float scale, void* out, float* lse, void* workspace, int64_t workspace_bytes,
+    kvc_stream stream);
+KVC_API kvc_status shared_kv_attention_topk(
+    const void* q, int64_t T, int32_t H, int64_t c, int32_t r, const void* nope, const void* rope,
+    int64_t cache_rows, float fp8_scale, const int64_t* key_start, const int64_t* n_visible,
+    const int32_t* idx, int64_t k, const void* win_nope, const void* win_rope, int64_t win_rows,
+    const int64_t* win_start, const int64_t* win_len, int64_t max_win, const float* sink,
+    float scale, void* out, float* lse, void* workspace, int64_t workspace_bytes,
+    kvc_stream stream);
+
 /* Name of the kernel that the calling host thread's most recent successful call launched
  * (e.g. "csa_small_m_kernel/c512", "window_tma_kernel", "fused_pair_kernel/csa"); "" before
  * the first launch.  Static storage, never NULL.  The record is per host thread and is

@@ -1524,10 +1524,11 @@ kvc_status read_and_clear_device_error(cudaStream_t st) {
   const bool index_error = read_and_clear_index_error(&failed);
   const unsigned int ix = read_and_clear_indexer_error(&failed);
   const unsigned int wx = read_and_clear_window_error(&failed);
+  const unsigned int ax = read_and_clear_attention_error(&failed);
   if (failed) return KVC_ERR_CUDA;
-  if (v || (ix & 1u) || (wx & 1u)) return KVC_ERR_TIMEOUT;
+  if (v || (ix & 1u) || (wx & 1u) || (ax & 1u)) return KVC_ERR_TIMEOUT;
   if (wx & 2u) return KVC_ERR_WORKSPACE;
-  return (index_error || (ix & 2u)) ? KVC_ERR_INDEX : KVC_OK;
+  return (index_error || (ix & 2u) || (ax & 2u)) ? KVC_ERR_INDEX : KVC_OK;
 }
 
 }  // namespace kvc

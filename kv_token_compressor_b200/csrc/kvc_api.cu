@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
 #include "../../include/kvc.h"
@@ -132,6 +133,74 @@ std::atomic<int> g_sync_check{0};
 kvc_status finish(kvc_status launched, cudaStream_t st) {
   if (launched != KVC_OK || g_sync_check.load(std::memory_order_relaxed) == 0) return launched;
   return kvc::read_and_clear_device_error(st);
+}
+
+// Shapes the attention kernels take: whole 8-channel chunks, and the FP8 and the bf16 part
+// each padded to 64-channel blocks within eight blocks.
+kvc_status attention_shape(int64_t T, int32_t H, int64_t c, int32_t r) {
+  if (H < 1 || c < 1 || r < 0 || r > c || c % 8 != 0 || r % 8 != 0) return KVC_ERR_SHAPE;
+  int64_t t = 0;
+  if (!mul_ok(T, H, &t) || !mul_ok(t, c, &t) || !mul_ok(t, 4, &t)) return KVC_ERR_SHAPE;
+  if ((c - r + 63) / 64 + (r + 63) / 64 > 8) return KVC_ERR_UNSUPPORTED;
+  return KVC_OK;
+}
+
+// Checks and launches a shared-KV attention problem (idx counts only with `listed`).
+kvc_status attention_call(const kvc::AttentionProblem& p, bool listed, int64_t workspace_bytes,
+                          cudaStream_t st) {
+  const int64_t r = p.r, cn = p.c - r;
+  const bool win = p.win_start != nullptr;
+  if (p.T < 0 || p.cache_rows < 0 || p.max_visible < 0 || (win && (p.win_rows < 0 || p.max_win < 0)))
+    return KVC_ERR_SHAPE;
+  kvc_status s = attention_shape(p.T, p.H, p.c, p.r);
+  if (s != KVC_OK) return s;
+  if (listed && (p.k < 1 || p.k > (int64_t(1) << 20))) return KVC_ERR_SHAPE;
+  if (!std::isfinite(p.fp8_scale) || !(p.fp8_scale > 0.f) || !std::isfinite(p.scale))
+    return KVC_ERR_SHAPE;
+  int64_t t = 0;
+  if (!mul_ok(p.cache_rows, p.c * 2, &t) || (win && !mul_ok(p.win_rows, p.c * 2, &t)) ||
+      (listed && (!mul_ok(p.T, p.k, &t) || !mul_ok(t, 4, &t))))
+    return KVC_ERR_SHAPE;
+  int64_t most = listed ? p.k : p.max_visible;
+  if (win && __builtin_add_overflow(most, p.max_win, &most)) return KVC_ERR_SHAPE;
+  if (p.T == 0) return KVC_OK;
+  if (most > (int64_t(1) << 31) - 1) return KVC_ERR_UNSUPPORTED;  // 32-bit row counts
+  const bool rows = p.cache_rows > 0, wrows = win && p.win_rows > 0;
+  if (!p.q || !p.out || !p.key_start || !p.n_visible || (listed && !p.idx)) return KVC_ERR_NULL;
+  if ((rows && ((cn > 0 && !p.nope) || (r > 0 && !p.rope))) || (win && !p.win_len) ||
+      (wrows && ((cn > 0 && !p.win_nope) || (r > 0 && !p.win_rope))))
+    return KVC_ERR_NULL;
+  const int64_t need = kvc::attention_workspace_bytes(p.T, p.H, p.c, p.r, most);
+  if (need > 0 && workspace_bytes < need) return KVC_ERR_SHAPE;
+  if (need > 0 && !p.workspace) return KVC_ERR_NULL;
+  const void* ps[14];
+  int np = 0;
+  bool align_ok = true;
+  auto use = [&](const void* ptr, uintptr_t a) {
+    ps[np++] = ptr;
+    align_ok = align_ok && aligned(ptr, a);
+  };
+  use(p.q, 16);
+  use(p.out, 16);
+  use(p.key_start, 8);
+  use(p.n_visible, 8);
+  if (rows && cn > 0) use(p.nope, 16);
+  if (rows && r > 0) use(p.rope, 16);
+  if (listed) use(p.idx, 4);
+  if (win) use(p.win_start, 8);
+  if (win) use(p.win_len, 8);
+  if (wrows && cn > 0) use(p.win_nope, 16);
+  if (wrows && r > 0) use(p.win_rope, 16);
+  if (p.sink) use(p.sink, 4);
+  if (p.lse) use(p.lse, 4);
+  if (need > 0) use(p.workspace, 256);
+  if (!align_ok) return KVC_ERR_ALIGN;
+  const uintptr_t qa = reinterpret_cast<uintptr_t>(p.q), oa = reinterpret_cast<uintptr_t>(p.out);
+  if ((qa > oa ? qa - oa : oa - qa) < static_cast<uintptr_t>(p.T * p.H * p.c * 2))
+    return KVC_ERR_POINTER;
+  s = check_ptrs(ps, np);
+  if (s != KVC_OK) return s;
+  return finish(kvc::launch_attention(p, st), st);
 }
 
 }  // namespace
@@ -927,6 +996,93 @@ kvc_status indexer_topk(const float* scores, int64_t ld, const int64_t* n_visibl
   kvc::TopkProblem p{scores, n_visible, T, max_visible, ld, k, out_idx, out_score};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return finish(kvc::launch_indexer_topk(p, st), st);
+}
+
+kvc_status partial_rope(const void* x, void* out, kvc_dtype dtype, int64_t T, int32_t H, int64_t c,
+                        int32_t r, const int64_t* pos, const float* inv_freq, int32_t layout,
+                        int32_t inverse, float magnitude, kvc_stream stream) {
+  if (!dtype_ok(dtype)) return KVC_ERR_DTYPE;
+  if (T < 0 || H < 1 || c < 0 || r < 0 || r > c || c % 8 != 0 || r % 8 != 0) return KVC_ERR_SHAPE;
+  if (layout != KVC_ROPE_INTERLEAVED && layout != KVC_ROPE_HALF) return KVC_ERR_SHAPE;
+  if ((inverse != 0 && inverse != 1) || !std::isfinite(magnitude)) return KVC_ERR_SHAPE;
+  int64_t bytes = 0;
+  if (!mul_ok(T, H, &bytes) || !mul_ok(bytes, c, &bytes) ||
+      !mul_ok(bytes, dtype == KVC_BF16 ? 2 : 4, &bytes))
+    return KVC_ERR_SHAPE;
+  if (T == 0 || c == 0 || (r == 0 && x == out)) return KVC_OK;
+  if (!x || !out || (r > 0 && (!pos || !inv_freq))) return KVC_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(out, 16) || (r > 0 && (!aligned(pos, 8) || !aligned(inv_freq, 4))))
+    return KVC_ERR_ALIGN;
+  const uintptr_t xa = reinterpret_cast<uintptr_t>(x), oa = reinterpret_cast<uintptr_t>(out);
+  const uintptr_t apart = xa > oa ? xa - oa : oa - xa;
+  if (apart != 0 && apart < static_cast<uintptr_t>(bytes)) return KVC_ERR_POINTER;
+  const void* ps[4] = {x, out, pos, inv_freq};
+  const kvc_status s = check_ptrs(ps, r > 0 ? 4 : 2);
+  if (s != KVC_OK) return s;
+  kvc::RopeProblem p{x, out, pos, inv_freq, T, c, H, r, dtype == KVC_BF16,
+                     layout == KVC_ROPE_HALF, inverse == 1, magnitude};
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return finish(kvc::launch_partial_rope(p, st), st);
+}
+
+kvc_status kvc_rope_frequencies(int32_t r, double base, double factor, double original_len,
+                                double beta_fast, double beta_slow, float* out) {
+  if (r < 8 || r % 8 != 0 || !std::isfinite(base) || !(base > 1.0) || !std::isfinite(factor) ||
+      !(factor >= 1.0))
+    return KVC_ERR_SHAPE;
+  double lo = 0.0, hi = 0.0;
+  if (factor > 1.0) {
+    if (!std::isfinite(original_len) || !(original_len > 0.0) || !std::isfinite(beta_fast) ||
+        !std::isfinite(beta_slow) || !(beta_slow > 0.0) || !(beta_fast > beta_slow))
+      return KVC_ERR_SHAPE;
+    auto pair_of = [&](double beta) {
+      return r * std::log(original_len / (6.283185307179586 * beta)) / (2.0 * std::log(base));
+    };
+    lo = std::fmax(std::floor(pair_of(beta_fast)), 0.0);
+    hi = std::fmax(std::fmin(std::ceil(pair_of(beta_slow)), r - 1.0), lo + 0.001);
+  }
+  if (!out) return KVC_ERR_NULL;
+  for (int32_t j = 0; j < r / 2; ++j) {
+    const double f = std::pow(base, -2.0 * j / r);
+    const double g =
+        factor > 1.0 ? std::fmin(std::fmax((j - lo) / (hi - lo), 0.0), 1.0) : 0.0;
+    out[j] = static_cast<float>(f * (1.0 - g) + f / factor * g);
+  }
+  return KVC_OK;
+}
+
+int64_t shared_kv_attention_workspace_bytes(int64_t T, int32_t H, int64_t c, int32_t r,
+                                            int64_t most_rows) {
+  if (T < 0 || most_rows < 0 || attention_shape(T, H, c, r) != KVC_OK) return -1;
+  if (T == 0) return 0;
+  return kvc::attention_workspace_bytes(T, H, c, r, most_rows);
+}
+
+kvc_status shared_kv_attention(const void* q, int64_t T, int32_t H, int64_t c, int32_t r,
+                               const void* nope, const void* rope, int64_t cache_rows,
+                               float fp8_scale, const int64_t* key_start, const int64_t* n_visible,
+                               int64_t max_visible, const void* win_nope, const void* win_rope,
+                               int64_t win_rows, const int64_t* win_start, const int64_t* win_len,
+                               int64_t max_win, const float* sink, float scale, void* out,
+                               float* lse, void* workspace, int64_t workspace_bytes,
+                               kvc_stream stream) {
+  kvc::AttentionProblem p{q, nope, rope, win_nope, win_rope, key_start, n_visible, nullptr,
+                          win_start, win_len, sink, out, lse, workspace, T, c, cache_rows,
+                          max_visible, 0, win_rows, max_win, H, r, fp8_scale, scale};
+  return attention_call(p, false, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+kvc_status shared_kv_attention_topk(
+    const void* q, int64_t T, int32_t H, int64_t c, int32_t r, const void* nope, const void* rope,
+    int64_t cache_rows, float fp8_scale, const int64_t* key_start, const int64_t* n_visible,
+    const int32_t* idx, int64_t k, const void* win_nope, const void* win_rope, int64_t win_rows,
+    const int64_t* win_start, const int64_t* win_len, int64_t max_win, const float* sink,
+    float scale, void* out, float* lse, void* workspace, int64_t workspace_bytes,
+    kvc_stream stream) {
+  kvc::AttentionProblem p{q, nope, rope, win_nope, win_rope, key_start, n_visible, idx,
+                          win_start, win_len, sink, out, lse, workspace, T, c, cache_rows,
+                          0, k, win_rows, max_win, H, r, fp8_scale, scale};
+  return attention_call(p, true, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int64_t kvc_topk_max_candidates(void) { return kvc::topk_max_candidates(); }

@@ -139,6 +139,46 @@ int64_t topk_max_candidates();
 // wait gave up, bit 1 a query's candidate window was out of range.
 unsigned int read_and_clear_indexer_error(bool* failed);
 
+// A validated partial-RoPE problem (partial_rope).
+struct RopeProblem {
+  const void* x;
+  void* out;
+  const int64_t* pos;
+  const float* inv_freq;
+  int64_t T, c;
+  int H, r;
+  bool bf16, half, inverse;
+  float magnitude;
+};
+kvc_status launch_partial_rope(const RopeProblem& p, cudaStream_t st);
+
+// A validated shared-KV attention problem (shared_kv_attention: idx == nullptr;
+// shared_kv_attention_topk: idx [T, k]).  win_start == nullptr: no window rows.
+struct AttentionProblem {
+  const void* q;  // [T, H, c] bf16
+  const void* nope;
+  const void* rope;
+  const void* win_nope;
+  const void* win_rope;
+  const int64_t* key_start;
+  const int64_t* n_visible;
+  const int32_t* idx;
+  const int64_t* win_start;
+  const int64_t* win_len;
+  const float* sink;
+  void* out;   // [T, H, c] bf16
+  float* lse;  // [T, H] or nullptr
+  void* workspace;
+  int64_t T, c, cache_rows, max_visible, k, win_rows, max_win;
+  int H, r;
+  float fp8_scale, scale;
+};
+kvc_status launch_attention(const AttentionProblem& p, cudaStream_t st);
+int64_t attention_workspace_bytes(int64_t T, int H, int64_t c, int r, int64_t most_rows);
+// Reads and clears the attention kernels' error word (no synchronisation): bit 0 a bounded
+// wait gave up, bit 1 a query's rows or a listed entry were out of range.
+unsigned int read_and_clear_attention_error(bool* failed);
+
 // The TMA-fed single-segment window kernel (dense HCA-style problems with m >= 32);
 // KVC_ERR_UNSUPPORTED when the problem or the device does not fit it (the caller then uses
 // the register-staged kernels).

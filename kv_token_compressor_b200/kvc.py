@@ -30,6 +30,9 @@ KVC_ERR_TOO_LARGE = 11
 # kvc_dtype
 KVC_F32 = 0
 KVC_BF16 = 1
+# kvc_rope_layout
+KVC_ROPE_INTERLEAVED = 0
+KVC_ROPE_HALF = 1
 
 # Every entry point the header declares, with its ctypes signature.
 _i64, _i32, _p = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p
@@ -70,6 +73,16 @@ SIGNATURES = {
                                                 _i64, _p]),
     "indexer_topk": (ctypes.c_int, [_p, _i64, _p, _i64, _i64, _i32, _p, _p, _p]),
     "kvc_topk_max_candidates": (_i64, []),
+    "partial_rope": (ctypes.c_int, [_p, _p, ctypes.c_int, _i64, _i32, _i64, _i32, _p, _p, _i32,
+                                    _i32, _f, _p]),
+    "kvc_rope_frequencies": (ctypes.c_int, [_i32, _d, _d, _d, _d, _d, _p]),
+    "shared_kv_attention_workspace_bytes": (_i64, [_i64, _i32, _i64, _i32, _i64]),
+    "shared_kv_attention": (ctypes.c_int, [_p, _i64, _i32, _i64, _i32, _p, _p, _i64, _f, _p, _p,
+                                           _i64, _p, _p, _i64, _p, _p, _i64, _p, _f, _p, _p, _p,
+                                           _i64, _p]),
+    "shared_kv_attention_topk": (ctypes.c_int, [_p, _i64, _i32, _i64, _i32, _p, _p, _i64, _f, _p,
+                                                _p, _p, _i64, _p, _p, _i64, _p, _p, _i64, _p, _f,
+                                                _p, _p, _p, _i64, _p]),
     "kvc_last_kernel": (ctypes.c_char_p, []),
     "hca_bias_workspace_bytes": (_i64, [_i64, _i32, ctypes.c_int]),
     "hca_prepare_bias": (ctypes.c_int, [_p, _i64, _i32, ctypes.c_int, _p, _i64, _p]),
@@ -620,6 +633,132 @@ def indexer_topk(scores, n_visible, k: int, max_visible: int, out_idx=None, out_
                             _stream(stream))
     _check(st, "indexer_topk")
     return out_idx, (out_score if want_scores else None)
+
+
+_ROPE_LAYOUTS = {"interleaved": KVC_ROPE_INTERLEAVED, "half": KVC_ROPE_HALF}
+
+
+def rope_frequencies(r: int, base: float = 10000.0, factor: float = 1.0,
+                     original_len: float = 4096.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                     device="cuda"):
+    """Rotary frequencies for r channels as a fp32 tensor [r / 2] on ``device``; factor > 1
+    stretches them by parts for contexts longer than original_len (include/kvc.h)."""
+    torch = _torch()
+    host = torch.empty(max(int(r) // 2, 0), dtype=torch.float32)
+    _check(lib().kvc_rope_frequencies(r, float(base), float(factor), float(original_len),
+                                      float(beta_fast), float(beta_slow), host.data_ptr()),
+           "kvc_rope_frequencies")
+    return host.to(device)
+
+
+def partial_rope(x, pos, inv_freq, r: int, layout: str = "interleaved", inverse: bool = False,
+                 magnitude: float = 1.0, out=None, stream=None):
+    """Rotate the last r channels of x [T, H, c] (bf16 or fp32) by pos[t] * inv_freq[j] (pos
+    int64 [T], inv_freq fp32 [r / 2]); inverse=True rotates back (also the gradient of the
+    forward call).  out=x works in place.  Returns out."""
+    torch = _torch()
+    if layout not in _ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(_ROPE_LAYOUTS)}, got {layout!r}")
+    T, H, c = x.shape
+    code = _dtype_code(x.dtype)
+    out = _out(out, (T, H, c), x.dtype, x)
+    ppos = pfreq = None
+    if r > 0:
+        _need("inv_freq", inv_freq, r // 2, torch.float32)
+        ppos, pfreq = _index(pos, T), _ptr(inv_freq)
+    st = lib().partial_rope(_ptr(x), _ptr(out), code, T, H, c, r, ppos, pfreq, _ROPE_LAYOUTS[layout],
+                            int(bool(inverse)), float(magnitude), _stream(stream))
+    _check(st, "partial_rope")
+    return out
+
+
+def shared_kv_attention_workspace_bytes(T: int, H: int, c: int, r: int, most_rows: int) -> int:
+    """Bytes of the attention workspace; most_rows = max_visible (or k) + max_win."""
+    return int(lib().shared_kv_attention_workspace_bytes(T, H, c, r, most_rows))
+
+
+def _cache_rows(nope, rope, c, r, what):
+    """Rows of a cache in the cache layout, after checking that both parts have them."""
+    torch = _torch()
+    rows = None
+    if c - r > 0:
+        if nope is None or nope.dim() != 2 or nope.shape[1] != c - r or nope.dtype not in (
+                torch.uint8, torch.float8_e4m3fn):
+            raise ValueError(f"{what}nope must be E4M3 bytes [rows, {c - r}]")
+        rows = nope.shape[0]
+    if r > 0:
+        if rope is None or rope.dim() != 2 or rope.shape[1] != r or rope.dtype != torch.bfloat16:
+            raise ValueError(f"{what}rope must be bf16 [rows, {r}]")
+        if rows is not None and rope.shape[0] != rows:
+            raise ValueError(f"{what}nope and {what}rope must have the same number of rows")
+        rows = rope.shape[0]
+    return rows
+
+
+def _attention(name, q, nope, rope, key_start, n_visible, extra, most, r, scale, fp8_scale, window,
+               sink, out, want_lse, lse, workspace, stream):
+    torch = _torch()
+    T, H, c = q.shape
+    _need("q", q, T * H * c, torch.bfloat16)
+    cn = c - r
+    known = 0 <= r <= c  # else the library reports r
+    rows = _cache_rows(nope, rope, c, r, "") if known else 0
+    wn = wr = ws = wl = None
+    wrows = max_win = 0
+    if window is not None:
+        wn, wr, ws, wl, max_win = window
+        wrows = _cache_rows(wn, wr, c, r, "window ") if known else 0
+    if sink is not None:
+        _need("sink", sink, H, torch.float32)
+    out = _out(out, (T, H, c), torch.bfloat16, q)
+    if want_lse or lse is not None:
+        lse = _out(lse, (T, H), torch.float32, q)
+    wargs = (_ptr(wn) if cn > 0 else None, _ptr(wr) if r > 0 else None, wrows,
+             _index(ws, T) if window is not None else None,
+             _index(wl, T) if window is not None else None, int(max_win))
+    nbytes = shared_kv_attention_workspace_bytes(T, H, c, r, most + int(max_win))
+    if workspace is None and nbytes > 0:
+        if stream is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        else:  # from the launching stream's pool: its reuse is ordered after the kernels
+            with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=q.device)):
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    st = getattr(lib(), name)(
+        _ptr(q), T, H, c, r, _ptr(nope) if cn > 0 else None, _ptr(rope) if r > 0 else None, rows,
+        float(fp8_scale), _index(key_start, T), _index(n_visible, T), *extra, *wargs, _ptr(sink),
+        float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
+        workspace.numel() * workspace.element_size() if workspace is not None else 0,
+        _stream(stream))
+    _check(st, name)
+    return out, lse
+
+
+def shared_kv_attention(q, nope, rope, key_start, n_visible, max_visible: int, r: int, scale: float,
+                        fp8_scale: float = 1.0, window=None, sink=None, out=None,
+                        want_lse: bool = False, lse=None, workspace=None, stream=None):
+    """Attention of q [T, H, c] bf16 over each query's visible cache entries (rows
+    key_start[t] .. + n_visible[t] - 1 of nope [rows, c - r] E4M3 / rope [rows, r] bf16, key and
+    value at once), with optional window rows (window = (win_nope, win_rope, win_start,
+    win_len, max_win)) and per-head sink logits (fp32 [H]).  Returns (out [T, H, c] bf16,
+    lse fp32 [T, H] or None)."""
+    return _attention("shared_kv_attention", q, nope, rope, key_start, n_visible,
+                      (int(max_visible),), int(max_visible), r, scale, fp8_scale, window, sink, out,
+                      want_lse, lse, workspace, stream)
+
+
+def shared_kv_attention_topk(q, nope, rope, key_start, n_visible, idx, r: int, scale: float,
+                             fp8_scale: float = 1.0, window=None, sink=None, out=None,
+                             want_lse: bool = False, lse=None, workspace=None, stream=None):
+    """shared_kv_attention over the listed entries idx [T, k] int32 (indexer_topk's output:
+    indices within the query's visible entries, -1 for none) instead of all visible ones."""
+    torch = _torch()
+    T = q.shape[0]
+    if idx.dtype != torch.int32 or idx.dim() != 2 or idx.shape[0] != T:
+        raise ValueError("idx must be int32 [T, k]")
+    k = idx.shape[1]
+    return _attention("shared_kv_attention_topk", q, nope, rope, key_start, n_visible,
+                      (_ptr(idx), k), k, r, scale, fp8_scale, window, sink, out, want_lse, lse,
+                      workspace, stream)
 
 
 def topk_max_candidates() -> int:
