@@ -28,9 +28,9 @@
 // accumulators of their own (S_n, S_r), because only S_n carries the row's power of two and
 // 1 / fp8_scale.  Both parts accumulate in fp32.
 //
-// Roles.  Warps 0-3 take the softmax, 4-7 store finished queries, 8-23 gather the rows (global
-// memory -> registers -> widened, swizzled shared memory), warp 24 issues the MMAs, warp 25
-// walks the segments (query, row tiles) of its CTA and posts them to the others.  A query's
+// Roles.  Warps 0-3 take the softmax, 4-7 store finished queries, 8-23 gather the rows (FP8:
+// global memory -> registers -> widened, swizzled shared memory; 26-27 copy the bf16 channels),
+// warp 24 issues the MMAs, warp 25 walks the segments (query, row tiles) of its CTA and posts them to the others.  A query's
 // tiles are split among CTAs when there are too few queries, and a second kernel joins the
 // parts in a fixed order.
 #include <cuda_fp16.h>
@@ -151,31 +151,15 @@ __device__ __forceinline__ Query query_of(const AttentionProblem& a, int64_t t) 
 
 // ------------------------------------------------------------------ PTX
 
-// TMEM <-> registers: 32 columns of a lane each; tmem_ld_rows: 16 lanes x 64 columns, lane i
+// TMEM <-> registers: 16 columns of a lane each (also tmem_ld16); tmem_ld_rows: 16 lanes x 64 columns, lane i
 // holding of rows i / 4 (v[4k], v[4k + 1]) and i / 4 + 8 (v[4k + 2], v[4k + 3]) the columns
 // 8k + 2 (i % 4) and the next.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
-      "%10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, "
-      "%26, %27, %28, %29, %30, %31}, [%32];"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
-        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
-        "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
-        "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
-        "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, "
-      "%8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, "
-      "%24, %25, %26, %27, %28, %29, %30, %31};" ::
-      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
-      "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]),
-      "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]),
-      "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]),
-      "f"(v[29]), "f"(v[30]), "f"(v[31]),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"f"(v[0]),
+      "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]),
+      "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]),
       "r"(taddr)
       : "memory");
 }
@@ -246,6 +230,7 @@ __device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity) {
 // Bounded wait of a whole warp; one answer for its lanes.  (No function call: calls do not go
 // with setmaxnreg.)
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+#pragma unroll 1
   for (uint32_t spins = 1;; ++spins) {
     if (__all_sync(0xffffffffu, try_wait_long(bar, parity))) return true;
     if (spins % 16 != 0) continue;
@@ -255,6 +240,20 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
     }
     if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
   }
+}
+// The same for one thread.
+__device__ __forceinline__ bool wait_thread(uint64_t* bar, uint32_t parity,
+                                            volatile int* abort_flag) {
+#pragma unroll 1
+  for (uint32_t spins = 1; !try_wait_long(bar, parity); ++spins) {
+    if (spins % 16 != 0) continue;
+    if (spins >= kSpinLimit) {
+      *abort_flag = 1;
+      atomicOr(&g_attention_error, 1u);
+    }
+    if (*abort_flag) return false;
+  }
+  return true;
 }
 // One lane of a converged warp, in the form the compiler knows to leave a single thread: the
 // MMAs' descriptors then need no per-lane handling (a lane == 0 test made each issue 4 times
@@ -294,100 +293,98 @@ struct Shared {
   }
 };
 
-// ------------------------------------------------------------------ row gather (16 warps)
+// ------------------------------------------------------------------ rows of a tile
 
-// Brings Q (once per segment) and the rows (tile by tile) into shared memory as the MMAs read
-// them: 128-byte rows of 64 16-bit channels, swizzled, FP8 widened to fp16.  Warp pw has rows
-// [4 pw, 4 pw + 4) of a tile (8 warps with 8 rows each took twice as long over a tile: the
-// gather is bound by the latency of its instructions).  FP8: a lane has the 8-channel chunks lane and lane + 32 of each
-// row (a warp reads 256 consecutive bytes); a tile's loads set out as soon as the registers of
-// the tile before are stored, and have until their place in the ring is free.  bf16: lane
-// group lane / 8 has row lane / 8, copied to its place as it is once that is free, after a
-// prefetch into L2 with the FP8 loads.
+// Walks the tiles of the CTA's segments for the warps that bring rows.  A lane has one row of
+// every tile, whose number may still be on its way after next() (a listed entry's load).
+struct RowCursor {
+  uint32_t sn = 0;     // segment records read
+  int j = 0, j1 = 0;   // next tile of the current segment
+  int item = -1;       // query and head group of the tile; -1: no more tiles
+  bool first = false;  // the tile begins its segment
+  int kind = 0;        // 0 none, 1 listed, 2 cache row, 3 window row
+  int raw = 0, listed = 0;
+
+  // The next tile, `r` of its rows.
+  __device__ __forceinline__ void next(const Args& a, const Shared& sh, int r) {
+    first = false;
+    while (j == j1) {  // the next segment with tiles
+      item = -1;
+      if (sn > 0) sh.arrive(kBSegEmpty + (sn - 1) % kSegs);
+      if (!sh.wait(kBSegFull + sn % kSegs, (sn / kSegs) & 1u)) return;
+      const Seg& q = sh.seg(sn);
+      ++sn;
+      if (q.t < 0) return;
+      j = q.j0;
+      j1 = q.j1;
+      first = true;
+    }
+    const Seg& q = sh.seg(sn - 1);
+    item = q.item;
+    const int e = j * kRows + r;
+    kind = e < q.n1 ? (a.p.idx ? 1 : 2) : e < q.n1 + q.n2 ? 3 : 0;
+    raw = e < q.n1 ? e : e - q.n1;
+    if (kind == 1) listed = __ldg(a.p.idx + q.t * a.p.k + e);  // (a select would wait for it)
+    ++j;
+  }
+  // The row's number in its array (*win: the window's), -1 for one that does not count.  The
+  // tile's segment record is still there: it is given back by the next() that leaves it.
+  __device__ __forceinline__ int64_t row(const Shared& sh, bool report, bool* win) {
+    const Seg& q = sh.seg(sn - 1);
+    *win = kind == 3;
+    if (kind == 0) return -1;
+    if (kind == 1) {
+      raw = listed;
+      if (raw < 0 || raw >= q.n_visible) {
+        if (raw != -1 && report) atomicOr(&g_attention_error, 2u);
+        return -1;
+      }
+    }
+    return (kind == 3 ? q.win_start : q.key_start) + raw;
+  }
+};
+
+// ------------------------------------------------------------------ FP8 gather (16 warps)
+
+// Brings Q (once per segment) and the rows' FP8 channels (tile by tile) into shared memory as
+// the MMAs read them: 128-byte rows of 64 16-bit channels, swizzled, widened to fp16.  Warp pw
+// has rows [4 pw, 4 pw + 4) of a tile, a lane the 8-channel chunks lane and lane + 32 of each
+// (a warp reads 256 consecutive bytes).  A tile's loads set out as soon as the registers of the
+// tile before are stored; its rows are prefetched into L2 one tile earlier.  (8 warps with 8
+// rows each took twice as long over a tile: the gather is bound by the latency of its
+// instructions.  Two register sets in turn need the code twice, which cost more than the
+// latency it hid.)
 __device__ __forceinline__ void gather(const Args& a, const Shared& sh) {
   uint8_t* smem = sh.smem;
   const int pw = (threadIdx.x >> 5) - kLoad0, lane = threadIdx.x & 31;
   const int lc = lane & 7, rsub = lane >> 3;
-  const int na = a.na, nr = a.nr;
-  int ch[2];      // channel of this lane's two FP8 chunks, -1: padding
-  bool in[2];
-  uint32_t at[2]; // their block in a tile
+  const int na = a.na;
+  int off[2];        // channel of this lane's two chunks
+  uint32_t keep[2];  // 0: padding
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int block = h * 4 + rsub;
-    in[h] = block < na;
-    ch[h] = in[h] ? channel_of(a, h * 256 + lane * 8) : -1;
-    at[h] = block * kAtom;
+    const int ch = h * 256 + lane * 8;
+    keep[h] = ch < a.cn ? ~0u : 0u;
+    off[h] = ch < a.cn ? ch : 0;
   }
-  // A tile whose row numbers are on their way: lane i (mod 4) has row pw * 4 + i.
-  int n_item = -1;      // query and head group; -1: no more tiles
-  bool n_first = false;
-  int kind = 0;         // 0 none, 1 listed (raw is an entry), 2 cache row, 3 window row
-  int raw = 0, listed = 0;
-  uint32_t sn = 0;      // segment records read
-  int j = 0, j1 = 0;    // next tile of the current segment
-  int item = -1, n1 = 0, n12 = 0, limit = 0;  // its query, cache rows, all rows, entries
-  int64_t key_start = 0, win_start = 0;
-  const int32_t* list = nullptr;
-  bool ended = false;
-  auto fetch = [&]() {
-    n_item = -1;
-    n_first = false;
-    if (j == j1) {  // the next segment with tiles
-      while (!ended) {
-        if (!sh.wait(kBSegFull + sn % kSegs, (sn / kSegs) & 1u)) {
-          ended = true;
-          break;
-        }
-        const Seg& q = sh.seg(sn);
-        j = q.j0;
-        j1 = q.j1;
-        ended = q.t < 0;
-        item = q.item;
-        n1 = q.n1;
-        n12 = q.n1 + q.n2;
-        limit = q.n_visible > 0x7fffffff ? 0x7fffffff : static_cast<int>(q.n_visible);
-        key_start = q.key_start;
-        win_start = q.win_start;
-        list = a.p.idx ? a.p.idx + q.t * a.p.k : nullptr;
-        sh.arrive(kBSegEmpty + sn % kSegs);
-        ++sn;
-        if (j1 > j) break;
-      }
-      if (ended) return;
-      n_first = true;
-    }
-    n_item = item;
-    const int e = j * kRows + pw * kOwn + (lane & (kOwn - 1));
-    kind = e < n1 ? (list ? 1 : 2) : e < n12 ? 3 : 0;
-    raw = e < n1 ? e : e - n1;
-    if (kind == 1) listed = __ldg(list + e);  // (not into raw: a select would wait for it)
-    ++j;
-  };
+  RowCursor cur;
   uint2 d[kOwn][2];
-  // lane i (mod 4): where row pw * 4 + i of the tile begins in the FP8 and the bf16 array (q,
-  // which is always there, for a row that does not count; what is read is dropped)
-  const uint8_t* np = nullptr;
-  const __nv_bfloat16* rp = nullptr;
   uint32_t bits = 0;  // which of the rows count
-  const int off[2] = {ch[0] < 0 ? 0 : ch[0], ch[1] < 0 ? 0 : ch[1]};
-  const uint32_t keep[2] = {ch[0] < 0 ? 0u : ~0u, ch[1] < 0 ? 0u : ~0u};
+  // lane i (mod 4): where row pw * 4 + i of the next tile begins (q, which is always there, for
+  // a row that does not count; what is read is dropped), and which of them count
+  const uint8_t *np = nullptr, *np_after = nullptr;
+  uint32_t nbits = 0, nbits_after = 0;
+  auto resolve = [&]() {  // ... of the tile after the next
+    bool win;
+    const int64_t row = cur.row(sh, lane < kOwn, &win);
+    nbits_after = __ballot_sync(0xffffffffu, row >= 0) & ((1u << kOwn) - 1u);
+    np_after = static_cast<const uint8_t*>(row < 0 ? a.p.q : win ? a.p.win_nope : a.p.nope);
+    if (row >= 0) np_after += row * a.cn;
+    // lanes 0-3 one 128-byte line of their row, lanes 4-7 the next, ...
+    if (row >= 0 && (lane >> 2) * 128 < a.cn) prefetch_l2(np_after + (lane >> 2) * 128);
+  };
   auto load = [&]() {
-    bool v = kind != 0;
-    if (kind == 1) {
-      raw = listed;
-      v = raw >= 0 && raw < limit;
-      if (!v && raw != -1 && lane < kOwn) atomicOr(&g_attention_error, 2u);
-    }
-    bits = __ballot_sync(0xffffffffu, v) & ((1u << kOwn) - 1u);
-    const bool win = kind == 3;
-    const int64_t row = (win ? win_start : key_start) + raw;
-    np = static_cast<const uint8_t*>(v ? (win ? a.p.win_nope : a.p.nope) : a.p.q);
-    rp = static_cast<const __nv_bfloat16*>(v ? (win ? a.p.win_rope : a.p.rope) : a.p.q);
-    if (v) {
-      np += row * a.cn;
-      rp += row * a.p.r;
-    }
+    bits = nbits;
     if (na > 0) {
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) {
@@ -397,38 +394,25 @@ __device__ __forceinline__ void gather(const Args& a, const Shared& sh) {
         d[i][1] = ld_chunk(p + off[1]);
       }
     }
-    if (lane < kOwn && v)
-      for (int k = 0; k < nr; ++k) prefetch_l2(rp + k * 64);
   };
   auto store = [&](uint32_t st) {
-    uint8_t* kb = smem + kSmK + st * kStage;
+    uint8_t* kb = smem + kSmK + st * kStage + rsub * kAtom;
     if (lane == 0) smem[kSmMask + st * kLoadWarps + pw] = static_cast<uint8_t>(bits);
-    if (nr > 0) {
-      const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(rp), rsub));
-      const int rr = pw * kOwn + rsub;
-      const uint32_t dst = smem_u32(kb) + na * kAtom + rr * 128 + ((lc ^ (rr & 7)) << 4);
-      const bool live = (bits >> rsub) & 1u;
-#pragma unroll 1
-      for (int k = 0; k < nr; ++k) {
-        const bool want = live && k * 64 + lc * 8 < a.p.r;
-        copy_chunk(dst + k * kAtom, want ? p + k * 64 + lc * 8 : a.p.q, want);
-      }
-    }
     if (na > 0) {
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) {
         const int rr = pw * kOwn + i;
-        const uint32_t place = rr * 128 + ((lc ^ (rr & 7)) << 4);
+        uint8_t* place = kb + rr * 128 + ((lc ^ (rr & 7)) << 4);
         const uint32_t live = 0u - ((bits >> i) & 1u);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint2 lo = widen4(d[i][h].x & live & keep[h]), hi = widen4(d[i][h].y & live & keep[h]);
-          if (in[h]) *reinterpret_cast<uint4*>(kb + at[h] + place) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+          const uint2 lo = widen4(d[i][h].x & live & keep[h]);
+          const uint2 hi = widen4(d[i][h].y & live & keep[h]);
+          if (h * 4 + rsub < na)
+            *reinterpret_cast<uint4*>(place + h * 4 * kAtom) = make_uint4(lo.x, lo.y, hi.x, hi.y);
         }
       }
     }
-    copies_done();
   };
   // Q of a segment: 4 rows per warp, FP8 channels to scaled fp16.
   auto load_q = [&](int item, uint32_t seg) {
@@ -437,12 +421,13 @@ __device__ __forceinline__ void gather(const Args& a, const Shared& sh) {
     const int heads = a.p.H - hg * kHeads;
     const __nv_bfloat16* qb =
         static_cast<const __nv_bfloat16*>(a.p.q) + (t * a.p.H + hg * kHeads) * a.p.c;
-    const int blocks = na + nr;
-    {
-      uint4 v[kOwn][2];
+    const int blocks = na + a.nr;
+#pragma unroll 1
+    for (int i0 = 0; i0 < kOwn; i0 += 2) {
+      uint4 v[2][2];
 #pragma unroll
-      for (int i = 0; i < kOwn; ++i) {
-        const int rr = pw * kOwn + i;
+      for (int i = 0; i < 2; ++i) {
+        const int rr = pw * kOwn + i0 + i;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int qc = h * 4 + rsub < blocks ? channel_of(a, h * 256 + lane * 8) : -1;
@@ -452,15 +437,15 @@ __device__ __forceinline__ void gather(const Args& a, const Shared& sh) {
         }
       }
 #pragma unroll
-      for (int i = 0; i < kOwn; ++i) {
-        const int rr = pw * kOwn + i;
+      for (int i = 0; i < 2; ++i) {
+        const int rr = pw * kOwn + i0 + i;
         uint32_t top = 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t w[4] = {v[i][h].x, v[i][h].y, v[i][h].z, v[i][h].w};
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (in[h]) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+            if (h * 4 + rsub < na) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
         }
         int e = static_cast<int>(__reduce_max_sync(0xffffffffu, top) >> 7);
         if (e == 255) e = 142;  // an infinity or NaN: no scaling
@@ -470,7 +455,7 @@ __device__ __forceinline__ void gather(const Args& a, const Shared& sh) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t w[4] = {v[i][h].x, v[i][h].y, v[i][h].z, v[i][h].w};
-          if (in[h]) {
+          if (h * 4 + rsub < na) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const __half2 hh = __floats2half2_rn(__uint_as_float(w[k] << 16) * mul,
@@ -479,39 +464,88 @@ __device__ __forceinline__ void gather(const Args& a, const Shared& sh) {
             }
           }
           if (h * 4 + rsub < blocks)
-            *reinterpret_cast<uint4*>(smem + kSmQ + at[h] + rr * 128 + ((lc ^ (rr & 7)) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(smem + kSmQ + (h * 4 + rsub) * kAtom + rr * 128 +
+                                      ((lc ^ (rr & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
     }
   };
 
   uint32_t gt = 0, seg = 0;
-  bool have = false;  // a tile's loads are in the registers
+  int item = -1;       // of the tile whose loads are under way
+  int n_item = -1;     // of the tile whose rows are known
+  bool first = false, n_first = false;
+  const int r = pw * kOwn + (lane & (kOwn - 1));
+  cur.next(a, sh, r);
   while (true) {
-    if (have) {
+    if (item >= 0) {
       const uint32_t st = gt % kStages;
-      if (!sh.wait(kBKEmpty + st, ((gt / kStages) & 1u) ^ 1u)) break;
-      store(st);
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      sh.arrive(kBKFull + st);
-      ++gt;
-      have = false;
-    }
-    if (n_item >= 0) {
-      if (n_first) {
-        if (!sh.wait(kBQEmpty, (seg & 1u) ^ 1u)) break;
-        load_q(n_item, seg);
+      if (first) {
+        if (!sh.wait(kBQEmpty, (seg & 1u) ^ 1u)) return;
+        load_q(item, seg);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         sh.arrive(kBQFull);
         ++seg;
       }
-      load();
-      have = true;
-    } else if (ended) {
-      break;
+      if (!sh.wait(kBKEmpty + st, ((gt / kStages) & 1u) ^ 1u)) return;
+      store(st);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      sh.arrive(kBKFull + st);
+      ++gt;
     }
-    fetch();
+    item = n_item;
+    first = n_first;
+    n_item = cur.item;
+    n_first = cur.first;
+    if (item < 0 && n_item < 0) return;
+    // a listed row's number, on its way since the last turn, is needed before the loads set
+    // out: the wait for it would be one for them too
+    if (n_item >= 0) resolve();
+    if (item >= 0) load();
+    np = np_after;
+    nbits = nbits_after;
+    if (n_item >= 0) cur.next(a, sh, r);
+  }
+}
+
+// ------------------------------------------------------------------ bf16 copy (2 warps)
+
+// The rows' bf16 channels go to their place as they are: a lane copies one row of a tile, 16
+// bytes at a time, once the place is free, after a prefetch into L2 one tile ahead.
+__device__ __forceinline__ void copy_bf16(const Args& a, const Shared& sh) {
+  const int r = threadIdx.x & 63;  // (the two warps begin at a multiple of 64 threads)
+  const int nr = a.nr;
+  RowCursor cur;
+  uint32_t gt = 0;
+  cur.next(a, sh, r);
+  while (cur.item >= 0) {
+    bool win;
+    const int64_t row = cur.row(sh, false, &win);
+    const bool live = row >= 0;
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(
+        !live ? a.p.q : win ? a.p.win_rope : a.p.rope);
+    if (live) {
+      src += row * a.p.r;
+      for (int ch = 0; ch < a.p.r; ch += 64) prefetch_l2(src + ch);
+    }
+    cur.next(a, sh, r);
+    const uint32_t st = gt % kStages;
+    if (!sh.wait(kBKEmpty + st, ((gt / kStages) & 1u) ^ 1u)) return;
+    const uint32_t dst =
+        smem_u32(sh.smem + kSmK + st * kStage + a.na * kAtom) + r * 128;
+#pragma unroll 1
+    for (int k = 0; k < nr; ++k) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const bool want = live && k * 64 + c * 8 < a.p.r;
+        copy_chunk(dst + k * kAtom + ((c ^ (r & 7)) << 4), want ? src + k * 64 + c * 8 : a.p.q,
+                   want);
+      }
+    }
+    copies_done();
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    sh.arrive(kBKFull + st);
+    ++gt;
   }
 }
 
@@ -614,13 +648,13 @@ __device__ __forceinline__ void softmax(const Args& a, const Shared& sh) {
         const float fb = __shfl_sync(0xffffffffu, f[1], (lane & 7) * 4);
         const float fl = lane & 8 ? fb : fa;  // of row lane % 16
 #pragma unroll 1
-        for (int c0 = 0; c0 < 256; c0 += 32) {
-          float v[32];
-          tmem_ld32(lane_addr + c0, v);
+        for (int c0 = 0; c0 < 256; c0 += 16) {
+          float v[16];
+          tmem_ld16(lane_addr + c0, v);
           tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 32; ++c) v[c] *= fl;
-          tmem_st32(lane_addr + c0, v);
+          for (int c = 0; c < 16; ++c) v[c] *= fl;
+          tmem_st16(lane_addr + c0, v);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -722,21 +756,21 @@ __device__ __forceinline__ void store_out_rows(const Args& a, const Shared& sh) 
         a.part_o + (static_cast<int64_t>(blockIdx.x * 2 + (part > 0 ? 1 : 0)) * kHeads + row) * a.p.c;
     if (nt == 0 && part >= 0) continue;
 #pragma unroll 1
-    for (int c0 = 0; c0 < 256 && c0 < slots; c0 += 32) {
-      float v[32];
+    for (int c0 = 0; c0 < 256 && c0 < slots; c0 += 16) {
+      float v[16];
       __syncwarp();
       if (nt > 0) {
-        tmem_ld32(lane_addr + c0, v);
+        tmem_ld16(lane_addr + c0, v);
         tmem_wait_ld();
       } else {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) v[c] = 0.f;
+        for (int c = 0; c < 16; ++c) v[c] = 0.f;
       }
       const int s0 = upper * 256 + c0;
       if (!live || s0 >= slots) continue;
       const float f = s0 < a.na * 64 ? f_nope : f_rope;
 #pragma unroll
-      for (int c = 0; c < 32; c += 8) {
+      for (int c = 0; c < 16; c += 8) {
         const int ch = channel_of(a, s0 + c);
         float o[8];
 #pragma unroll
@@ -775,15 +809,7 @@ __device__ __forceinline__ void issue_mmas(const Args& a, const Shared& sh) {
   const uint64_t pd = smem_desc(smem_u32(sh.smem + kSmP), 16, 1024, 2);
   const uint32_t is_n = idesc(false, false, kRows), is_r = idesc(true, false, kRows);
   auto wait = [&](int bar, uint32_t parity) {
-    for (uint32_t spins = 1; !try_wait_long(bars + bar, parity); ++spins) {
-      if (spins % 16 != 0) continue;
-      if (spins >= kSpinLimit) {
-        *sh.abort_flag = 1;
-        atomicOr(&g_attention_error, 1u);
-      }
-      if (*sh.abort_flag) return false;
-    }
-    return true;
+    return wait_thread(bars + bar, parity, sh.abort_flag);
   };
   uint32_t sn = 0;                // segment records read
   int j = 0, j1 = 0;              // tiles of the current segment
@@ -818,6 +844,7 @@ __device__ __forceinline__ void issue_mmas(const Args& a, const Shared& sh) {
       if (!ok) break;
       tc_fence_after();
       const uint32_t dt = tmem + kColS + 64 * b;
+#pragma unroll 1
       for (int at = 0; at < blocks; ++at) {
         const bool r = at >= na;
 #pragma unroll
@@ -842,7 +869,7 @@ __device__ __forceinline__ void issue_mmas(const Args& a, const Shared& sh) {
       if (!ok) break;
       tc_fence_after();
       const uint64_t pn = pd + ((b * 2 * kAtom) >> 4), pr = pn + (kAtom >> 4);
-#pragma unroll
+#pragma unroll 1
       for (int ks = 0; ks < kRows / 16; ++ks) {
         const uint64_t d = vd + ((st * kStage + ks * 16 * 128) >> 4);
         const uint64_t an = pn + ((ks * 32) >> 4), ar = pr + ((ks * 32) >> 4);
@@ -938,13 +965,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1;  // commits, the scheduler
-      if (i >= kBKFull && i < kBKFull + kStages) count = kLoadWarps;
+      if (i >= kBKFull && i < kBKFull + kStages) count = kLoadWarps + 2;
       if (i == kBQFull) count = kLoadWarps;
       if (i >= kBSFree && i < kBSFree + 2) count = kSoftWarps;
       if (i >= kBPFull && i < kBPFull + 2) count = kSoftWarps;
       if (i == kBOFree) count = kStoreWarps;
       if (i >= kBLFull && i < kBLFull + kSegs) count = kSoftWarps;
-      if (i >= kBSegEmpty && i < kBSegEmpty + kSegs) count = kMmaWarp + 1;
+      if (i >= kBSegEmpty && i < kBSegEmpty + kSegs) count = kMmaWarp + 3;
       mbar_init(sh.bars + i, count);
     }
     *sh.abort_flag = 0;
@@ -977,6 +1004,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       if (elect_one()) issue_mmas(a, sh);
     } else if (warp == kMmaWarp + 1) {
       if (elect_one()) schedule(a, sh);
+    } else {
+      copy_bf16(a, sh);
     }
   }
 
