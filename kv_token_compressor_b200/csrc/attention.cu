@@ -952,6 +952,7 @@ __device__ __forceinline__ void schedule(const Args& a, const Shared& sh) {
 
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(1024) uint8_t smem[];
+  griddep_launch_dependents();  // the join, which waits for this grid's end before it reads
   if ((smem_u32(smem) & 1023u) != 0) {  // the 128-byte swizzle counts on it
     if (threadIdx.x == 0) atomicOr(&g_attention_error, 1u);
     return;
@@ -1020,67 +1021,186 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 
 // ------------------------------------------------------------------ joining the parts
 
-constexpr int kJoinThreads = 128;
+// A query (of one group of heads) whose units lie in several CTAs has that many parts to join:
+//     out = sum_p 2^(m_p - M) O_p / D,  D = sum_p 2^(m_p - M) l_p (+ sink),  M = max m_p,
+// in an order that the plan alone fixes.  A query with few parts takes a warp for each of its
+// heads, one with many a block of 8 groups of 128 threads that take every eighth part.  Bound
+// by the parts' bytes (fp32, from L2 as a rule) and by three dependent round trips, so all of
+// it should be resident at once.  (A block for every head of every CTA boundary, most of
+// them idle, took 26 to 40 us.)
+constexpr int kMaxParts = 160;   // CTAs, with room
+constexpr int kFewParts = 8;
+constexpr int kJoinWarps = 8;
 
-// A query whose units begin in CTA k - 1 and go on in CTA k (and perhaps further) was split:
-// block (k, head) adds its parts in CTA order.
-__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Args a) {
-  const int64_t k = blockIdx.x, U = a.units, C = a.ctas;
+struct Split {
+  int kf, parts;    // first CTA, number of parts
+  int64_t t;
+  int hg;
+  bool ok;
+};
+// The x-th query that may be split: with fewer queries than CTAs the x-th one, else the one that
+// CTA x ends in and CTA x + 1 goes on with, if CTA x is its first.
+__device__ __forceinline__ Split split_of(const Args& a, int64_t x) {
+  const int64_t U = a.units, C = a.ctas;
   const int tpi = a.tiles_per_item;
-  const int64_t lo = k * U / C;
-  const int64_t item = lo / tpi;
-  if (lo == item * tpi) return;
+  Split s;
+  s.ok = false;
+  int64_t item = x;
+  if (a.items >= C) {
+    const int64_t lo = (x + 1) * U / C;
+    item = lo / tpi;
+    if (lo == item * tpi) return s;
+  }
   const int64_t kf = ((item * tpi + 1) * C - 1) / U;
-  if (kf != k - 1) return;
-  const int64_t kl = ((item + 1) * tpi * C - 1) / U;
-  const int64_t t = item / a.groups;
-  const int hg = static_cast<int>(item - t * a.groups);
-  const int row = blockIdx.y, head = hg * kHeads + row;
-  if (head >= a.p.H || !query_of(a.p, t).ok) return;
-  auto slot = [&](int64_t c) { return (c * 2 + (c == kf ? 1 : 0)) * kHeads + row; };
+  if (a.items >= C && kf != x) return s;
+  s.kf = static_cast<int>(kf);
+  s.parts = static_cast<int>(((item + 1) * tpi * C - 1) / U - kf) + 1;
+  s.t = item / a.groups;
+  s.hg = static_cast<int>(item - s.t * a.groups);
+  s.ok = s.parts > 1 && query_of(a.p, s.t).ok;
+  return s;
+}
+// Row of part p in the workspace: slot 1 of the first CTA, slot 0 of the others.
+__device__ __forceinline__ int64_t part_row(const Split& s, int p, int row) {
+  return static_cast<int64_t>((s.kf + p) * 2 + (p == 0 ? 1 : 0)) * kHeads + row;
+}
+// Weight of a part with maximum m and sum l: a part without a row has l = 0, and its O is not
+// written; NaN scores leave l NaN, and perhaps m = -inf.
+__device__ __forceinline__ float part_weight(float2 ml, float ref) {
+  return ml.y == 0.f ? 0.f : ml.y != ml.y ? ml.y : ex2_ftz(ml.x - ref);
+}
+__device__ __forceinline__ float4 fma4(float4 v, float w, float4 o) {
+  return make_float4(fmaf(v.x, w, o.x), fmaf(v.y, w, o.y), fmaf(v.z, w, o.z), fmaf(v.w, w, o.w));
+}
+__device__ __forceinline__ void store4(const Args& a, int64_t out_row, int ch, float4 o, float inv) {
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.p.out) + out_row * a.p.c + ch) =
+      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+}
+__device__ __forceinline__ void store_lse(const Args& a, int64_t out_row, bool any, float sink,
+                                          float ref, float den) {
+  if (a.p.lse) a.p.lse[out_row] = any ? ref * 0.6931471805599453f + logf(den) : sink;
+}
+
+__global__ void __launch_bounds__(32 * kJoinWarps) attention_join_few_kernel(const Args a) {
+  __shared__ Split sp;
+  griddep_wait();  // the parts are complete
+  if (threadIdx.x == 0) sp = split_of(a, blockIdx.x);
+  __syncthreads();
+  const int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int head = sp.hg * kHeads + row;
+  if (!sp.ok || head >= a.p.H) return;
+  const int parts = sp.parts;  // at most kFewParts
+  const int64_t out_row = sp.t * a.p.H + head;
   const float sink = a.p.sink ? a.p.sink[head] : -INFINITY;
-  const float sink2 = sink * kLog2e;
-  float M = sink2;
-  bool nan = false, rows = false;
-  for (int64_t c = kf; c <= kl; ++c) {
-    const float2 ml = a.part_ml[slot(c)];
-    M = fmaxf(M, ml.x);
-    nan = nan || ml.y != ml.y;
-    rows = rows || ml.y != 0.f;
-  }
-  float den = 0.f;
+  float2 ml = make_float2(-INFINITY, 0.f);
+  if (lane < parts) ml = a.part_ml[part_row(sp, lane, row)];
+  float M = ml.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  M = fmaxf(M, sink * kLog2e);
   const float ref = M == -INFINITY ? 0.f : M;
-  for (int64_t c = kf; c <= kl; ++c) {
-    const float2 ml = a.part_ml[slot(c)];
-    if (ml.y != 0.f) den += ml.y * ex2_ftz(ml.x - ref);
-  }
-  if (a.p.sink) den += ex2_ftz(sink2 - ref);
-  if (nan) den = NAN;
-  if (threadIdx.x == 0 && a.p.lse)
-    a.p.lse[t * a.p.H + head] = !rows ? sink : ref * 0.6931471805599453f + logf(den);
+  const float w = part_weight(ml, ref);
+  float den = ml.y == 0.f ? 0.f : w * ml.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+  if (a.p.sink) den += ex2_ftz(sink * kLog2e - ref);
+  const bool any = __any_sync(0xffffffffu, ml.y != 0.f);
+  if (lane == 0) store_lse(a, out_row, any, sink, ref, den);
   const float inv = den != 0.f ? 1.f / den : 0.f;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.p.out) + (t * a.p.H + head) * a.p.c;
-  for (int ch = threadIdx.x * 4; ch < a.p.c; ch += kJoinThreads * 4) {
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t c = kf; c <= kl; ++c) {
-      const int64_t s = slot(c);
-      const float2 ml = a.part_ml[s];
-      if (ml.y == 0.f) continue;  // the part had no row: its O is not written
-      const float f = ex2_ftz(ml.x - ref);
-      const float4 v = *reinterpret_cast<const float4*>(a.part_o + s * a.p.c + ch);
-      o.x = fmaf(v.x, f, o.x);
-      o.y = fmaf(v.y, f, o.y);
-      o.z = fmaf(v.z, f, o.z);
-      o.w = fmaf(v.w, f, o.w);
+  for (int c0 = 0; c0 < a.p.c; c0 += 512) {
+    float4 o[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int p = 0; p < parts; ++p) {
+      const float wp = __shfl_sync(0xffffffffu, w, p);
+      if (wp == 0.f) continue;  // nothing to add (and perhaps nothing written)
+      const float* src = a.part_o + part_row(sp, p, row) * a.p.c + c0 + lane * 4;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (c0 + q * 128 + lane * 4 < a.p.c)
+          o[q] = fma4(*reinterpret_cast<const float4*>(src + q * 128), wp, o[q]);
     }
-    *reinterpret_cast<uint2*>(out + ch) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (c0 + q * 128 + lane * 4 < a.p.c) store4(a, out_row, c0 + q * 128 + lane * 4, o[q], inv);
+  }
+}
+
+constexpr int kJoinGroups = 8;
+__global__ void __launch_bounds__(128 * kJoinGroups) attention_join_many_kernel(const Args a) {
+  constexpr int G = kJoinGroups;
+  __shared__ Split sp;
+  __shared__ float weight[kMaxParts], red[3][4 * G];
+  __shared__ float4 sums[G - 1][128];
+  const int tid = threadIdx.x, row = blockIdx.y;
+  griddep_wait();  // the parts are complete
+  if (tid == 0) sp = split_of(a, blockIdx.x);
+  __syncthreads();
+  const int head = sp.hg * kHeads + row;
+  if (!sp.ok || head >= a.p.H) return;
+  const int parts = sp.parts;
+  const int64_t out_row = sp.t * a.p.H + head;
+  const float sink = a.p.sink ? a.p.sink[head] : -INFINITY;
+  // every part's m and l at once (there are fewer parts than threads)
+  float2 ml = make_float2(-INFINITY, 0.f);
+  if (tid < parts) ml = a.part_ml[part_row(sp, tid, row)];
+  float M = ml.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if ((tid & 31) == 0) red[0][tid >> 5] = M;
+  __syncthreads();
+  M = sink * kLog2e;
+#pragma unroll
+  for (int w = 0; w < 4 * G; ++w) M = fmaxf(M, red[0][w]);
+  const float ref = M == -INFINITY ? 0.f : M;
+  const float wt = part_weight(ml, ref);
+  if (tid < parts) weight[tid] = wt;
+  float den = ml.y == 0.f ? 0.f : wt * ml.y;
+  float any = ml.y == 0.f ? 0.f : 1.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    den += __shfl_xor_sync(0xffffffffu, den, o);
+    any += __shfl_xor_sync(0xffffffffu, any, o);
+  }
+  if ((tid & 31) == 0) {
+    red[1][tid >> 5] = den;
+    red[2][tid >> 5] = any;
+  }
+  __syncthreads();
+  den = a.p.sink ? ex2_ftz(sink * kLog2e - ref) : 0.f;
+  any = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4 * G; ++w) {
+    den += red[1][w];
+    any += red[2][w];
+  }
+  if (tid == 0) store_lse(a, out_row, any != 0.f, sink, ref, den);
+  const float inv = den != 0.f ? 1.f / den : 0.f;
+  const int g = tid >> 7, lane = tid & 127;
+  const int ch = lane * 4;  // c is at most 512
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (ch < a.p.c) {
+#pragma unroll 4
+    for (int p = g; p < parts; p += G) {
+      const float w = weight[p];
+      if (w == 0.f) continue;
+      o = fma4(*reinterpret_cast<const float4*>(a.part_o + part_row(sp, p, row) * a.p.c + ch), w, o);
+    }
+  }
+  if (g > 0) sums[g - 1][lane] = o;
+  __syncthreads();
+  if (g == 0 && ch < a.p.c) {
+#pragma unroll
+    for (int i = 0; i < G - 1; ++i) o = fma4(sums[i][lane], 1.f, o);
+    store4(a, out_row, ch, o, inv);
   }
 }
 
 // ------------------------------------------------------------------ launch
 
 constexpr int kMaxCtas = 148;        // SMs: one CTA each
+static_assert(kMaxCtas <= kMaxParts, "a query may be split among all CTAs");
 constexpr int kMinTiles = 2;         // tiles per CTA below which a query is not split further
 constexpr int64_t kStridedItems = 8; // items per CTA from which queries are never split
 
@@ -1142,9 +1262,26 @@ kvc_status launch_attention(const AttentionProblem& p, cudaStream_t st) {
   attention_kernel<<<pl.ctas, kThreads, kSmem, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return KVC_ERR_CUDA;
   const bool whole = pl.units % pl.ctas == 0 && (pl.units / pl.ctas) % pl.tiles_per_item == 0;
-  if (!pl.strided && !whole) {  // some query is split
-    attention_join_kernel<<<dim3(pl.ctas, p.H < kHeads ? p.H : kHeads), kJoinThreads, 0, st>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return KVC_ERR_CUDA;
+  if (!pl.strided && !whole && pl.tiles_per_item > 1) {  // some query is split
+    // launched as a programmatic dependent: it may set up while the parts are still made
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    const int rows = p.H < kHeads ? p.H : kHeads;
+    const int64_t splits = pl.items < pl.ctas ? pl.items : pl.ctas - 1;
+    // the most CTAs a query's units can lie in
+    const int64_t parts = (pl.tiles_per_item - 2) / (pl.units / pl.ctas) + 2;
+    const bool few = parts <= kFewParts;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(splits),
+                       static_cast<unsigned>(few ? ceil_div(rows, kJoinWarps) : rows), 1);
+    cfg.blockDim = dim3(few ? 32 * kJoinWarps : 128 * kJoinGroups, 1, 1);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, few ? attention_join_few_kernel : attention_join_many_kernel, a) !=
+        cudaSuccess)
+      return KVC_ERR_CUDA;
   }
   last_kernel() = "attention_kernel";
   return KVC_OK;
