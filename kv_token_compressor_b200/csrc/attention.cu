@@ -119,14 +119,25 @@ constexpr uint32_t kUpper = 16u << 16;
 
 struct Args {
   AttentionProblem p;
-  int64_t items, units;     // (query, head group); units = items x tiles_per_item
-  int tiles_per_item, groups, ctas;
+  int items, tiles_per_item;  // an item: a query and a group of heads
+  int groups, ctas;
+  int per_cta, extra;       // units (items x tiles_per_item): per CTA, one more for the first `extra`
   int na, nr;               // 64-channel blocks: FP8, then bf16
   int cn;                   // FP8 channels
   bool strided;             // whole items, CTA by CTA (no splits)
-  float* part_o;            // [ctas][2][kHeads][c] fp32
+  bool wide_out;            // 32-byte stores to out are aligned (16 channels at a multiple of 16)
+  float4* part_o;           // [ctas][2][c / 4][kHeads] fp32, 4 channels each
   float2* part_ml;          // [ctas][2][kHeads] (m, l)
 };
+
+// First unit of CTA k, and the CTA that has unit u.
+__device__ __forceinline__ int first_unit(const Args& a, int k) {
+  return k * a.per_cta + (k < a.extra ? k : a.extra);
+}
+__device__ __forceinline__ int cta_of(const Args& a, int u) {
+  const int long_ones = a.extra * (a.per_cta + 1);
+  return u < long_ones ? u / (a.per_cta + 1) : a.extra + (u - long_ones) / a.per_cta;
+}
 
 // The rows of query t.
 struct Query {
@@ -195,6 +206,11 @@ __device__ __forceinline__ uint2 widen4(uint32_t w) {
       : "=r"(v.x), "=r"(v.y)
       : "r"(w));
   return v;
+}
+__device__ __forceinline__ void st_global32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 // 16 bytes from global to shared memory, asynchronously; zeros if not wanted.
 __device__ __forceinline__ void copy_chunk(uint32_t dst, const void* p, bool want) {
@@ -415,12 +431,22 @@ __device__ __forceinline__ void gather(const Args& a, const Shared& sh) {
     }
   };
   // Q of a segment: 4 rows per warp, FP8 channels to scaled fp16.
+  auto q_rows = [&](int item, int* heads) {
+    const int t = item / a.groups, hg = item - t * a.groups;
+    *heads = a.p.H - hg * kHeads;
+    return static_cast<const __nv_bfloat16*>(a.p.q) +
+           (static_cast<int64_t>(t) * a.p.H + hg * kHeads) * a.p.c;
+  };
+  // A line of 64 channels for every lane: this warp's 4 rows are in L2 when their turn comes.
+  auto prefetch_q = [&](int item) {
+    int heads;
+    const __nv_bfloat16* qb = q_rows(item, &heads);
+    const int rr = pw * kOwn + rsub;
+    if (rr < heads && lc * 64 < a.p.c) prefetch_l2(qb + rr * a.p.c + lc * 64);
+  };
   auto load_q = [&](int item, uint32_t seg) {
-    const int64_t t = item / a.groups;
-    const int hg = item - static_cast<int>(t) * a.groups;
-    const int heads = a.p.H - hg * kHeads;
-    const __nv_bfloat16* qb =
-        static_cast<const __nv_bfloat16*>(a.p.q) + (t * a.p.H + hg * kHeads) * a.p.c;
+    int heads;
+    const __nv_bfloat16* qb = q_rows(item, &heads);
     const int blocks = na + a.nr;
 #pragma unroll 1
     for (int i0 = 0; i0 < kOwn; i0 += 2) {
@@ -477,6 +503,7 @@ __device__ __forceinline__ void gather(const Args& a, const Shared& sh) {
   bool first = false, n_first = false;
   const int r = pw * kOwn + (lane & (kOwn - 1));
   cur.next(a, sh, r);
+  if (cur.item >= 0) prefetch_q(cur.item);
   while (true) {
     if (item >= 0) {
       const uint32_t st = gt % kStages;
@@ -504,7 +531,10 @@ __device__ __forceinline__ void gather(const Args& a, const Shared& sh) {
     if (item >= 0) load();
     np = np_after;
     nbits = nbits_after;
-    if (n_item >= 0) cur.next(a, sh, r);
+    if (n_item >= 0) {
+      cur.next(a, sh, r);
+      if (cur.first && cur.item >= 0) prefetch_q(cur.item);
+    }
   }
 }
 
@@ -752,8 +782,11 @@ __device__ __forceinline__ void store_out_rows(const Args& a, const Shared& sh) 
     }
     const float f_nope = f_rope * inv_fp8;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.p.out) + (t * a.p.H + head) * a.p.c;
-    float* po =
-        a.part_o + (static_cast<int64_t>(blockIdx.x * 2 + (part > 0 ? 1 : 0)) * kHeads + row) * a.p.c;
+    // (a part lies with its rows side by side, as the lanes have them)
+    float4* po = a.part_o +
+                 static_cast<int64_t>(blockIdx.x * 2 + (part > 0 ? 1 : 0)) * (a.p.c / 4) * kHeads +
+                 row;
+    const bool wide = a.wide_out;
     if (nt == 0 && part >= 0) continue;
 #pragma unroll 1
     for (int c0 = 0; c0 < 256 && c0 < slots; c0 += 16) {
@@ -770,20 +803,25 @@ __device__ __forceinline__ void store_out_rows(const Args& a, const Shared& sh) 
       if (!live || s0 >= slots) continue;
       const float f = s0 < a.na * 64 ? f_nope : f_rope;
 #pragma unroll
-      for (int c = 0; c < 16; c += 8) {
-        const int ch = channel_of(a, s0 + c);
-        float o[8];
+      for (int e = 0; e < 16; ++e) v[e] *= f;
+      const int ch = channel_of(a, s0), ch8 = channel_of(a, s0 + 8);
+      if (part < 0) {
+        uint32_t o[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = v[c + e] * f;
-        if (ch >= 0) {
-          if (part < 0) {
-            *reinterpret_cast<uint4*>(out + ch) =
-                make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
-                           pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
-          } else {
-            *reinterpret_cast<float4*>(po + ch) = make_float4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<float4*>(po + ch + 4) = make_float4(o[4], o[5], o[6], o[7]);
-          }
+        for (int e = 0; e < 8; ++e) o[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+        if (wide && ch8 >= 0) {  // a whole 32-byte sector: twice as fast as two halves
+          st_global32(out + ch, o);
+        } else {
+          if (ch >= 0) *reinterpret_cast<uint4*>(out + ch) = make_uint4(o[0], o[1], o[2], o[3]);
+          if (ch8 >= 0) *reinterpret_cast<uint4*>(out + ch8) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+          const int c4 = e < 8 ? ch : ch8;
+          if (c4 >= 0)
+            po[static_cast<int64_t>(c4 / 4 + (e & 4) / 4) * kHeads] =
+                make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
         }
       }
     }
@@ -900,28 +938,27 @@ __device__ __forceinline__ void issue_mmas(const Args& a, const Shared& sh) {
 __device__ __forceinline__ void schedule(const Args& a, const Shared& sh) {
   Seg* segs = reinterpret_cast<Seg*>(sh.smem + kSmSeg);
   const int cta = blockIdx.x;
-  int64_t at = a.strided ? cta : cta * a.units / a.ctas;
-  const int64_t end = a.strided ? a.items : (cta + 1) * a.units / a.ctas;
+  int at = a.strided ? cta : first_unit(a, cta);
+  const int end = a.strided ? a.items : first_unit(a, cta + 1);
   const int tpi = a.tiles_per_item;
   for (uint32_t sn = 0;; ++sn) {
     Seg q;
     q.t = -1;
     q.j0 = q.j1 = 0;
     if (at < end) {
-      int64_t item = at;
-      int f0 = 0, f1 = tpi;
+      int item = at, f0 = 0, f1 = tpi;
       if (a.strided) {
         at += a.ctas;
       } else {
         item = at / tpi;
-        f0 = static_cast<int>(at - item * tpi);
-        if (end - at < tpi - f0) f1 = f0 + static_cast<int>(end - at);
+        f0 = at - item * tpi;
+        if (end - at < tpi - f0) f1 = f0 + end - at;
         at += f1 - f0;
       }
       q.part = (f0 == 0 && f1 == tpi) ? -1 : (f0 > 0 ? 0 : 1);
-      q.item = static_cast<int>(item);
+      q.item = item;
       q.t = item / a.groups;
-      q.hg = static_cast<int>(item - q.t * a.groups);
+      q.hg = item - static_cast<int>(q.t) * a.groups;
       const Query y = query_of(a.p, q.t);
       q.key_start = y.key_start;
       q.win_start = y.win_start;
@@ -931,8 +968,8 @@ __device__ __forceinline__ void schedule(const Args& a, const Shared& sh) {
       q.ok = y.ok;
       // a query shorter than the longest spreads its tiles over its CTAs alike
       const int nt = (y.n1 + y.n2 + kRows - 1) / kRows;
-      q.j0 = static_cast<int>(static_cast<int64_t>(f0) * nt / tpi);
-      q.j1 = static_cast<int>(static_cast<int64_t>(f1) * nt / tpi);
+      q.j0 = f0 == 0 ? 0 : static_cast<int>(static_cast<int64_t>(f0) * nt / tpi);
+      q.j1 = f1 == tpi ? nt : static_cast<int>(static_cast<int64_t>(f1) * nt / tpi);
     }
     const long long t0 = clock64();
     while (!mbar_try_wait(sh.bars + kBSegEmpty + sn % kSegs, ((sn / kSegs) & 1u) ^ 1u)) {
@@ -1030,7 +1067,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 // them idle, took 26 to 40 us.)
 constexpr int kMaxParts = 160;   // CTAs, with room
 constexpr int kFewParts = 8;
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 4;
 
 struct Split {
   int kf, parts;    // first CTA, number of parts
@@ -1040,29 +1077,27 @@ struct Split {
 };
 // The x-th query that may be split: with fewer queries than CTAs the x-th one, else the one that
 // CTA x ends in and CTA x + 1 goes on with, if CTA x is its first.
-__device__ __forceinline__ Split split_of(const Args& a, int64_t x) {
-  const int64_t U = a.units, C = a.ctas;
+__device__ __forceinline__ Split split_of(const Args& a, int x) {
   const int tpi = a.tiles_per_item;
   Split s;
   s.ok = false;
-  int64_t item = x;
-  if (a.items >= C) {
-    const int64_t lo = (x + 1) * U / C;
+  int item = x;
+  if (a.items >= a.ctas) {
+    const int lo = first_unit(a, x + 1);
     item = lo / tpi;
     if (lo == item * tpi) return s;
   }
-  const int64_t kf = ((item * tpi + 1) * C - 1) / U;
-  if (a.items >= C && kf != x) return s;
-  s.kf = static_cast<int>(kf);
-  s.parts = static_cast<int>(((item + 1) * tpi * C - 1) / U - kf) + 1;
+  s.kf = cta_of(a, item * tpi);
+  if (a.items >= a.ctas && s.kf != x) return s;
+  s.parts = cta_of(a, item * tpi + tpi - 1) - s.kf + 1;
   s.t = item / a.groups;
-  s.hg = static_cast<int>(item - s.t * a.groups);
+  s.hg = item - static_cast<int>(s.t) * a.groups;
   s.ok = s.parts > 1 && query_of(a.p, s.t).ok;
   return s;
 }
-// Row of part p in the workspace: slot 1 of the first CTA, slot 0 of the others.
-__device__ __forceinline__ int64_t part_row(const Split& s, int p, int row) {
-  return static_cast<int64_t>((s.kf + p) * 2 + (p == 0 ? 1 : 0)) * kHeads + row;
+// Part p of the workspace: slot 1 of the first CTA, slot 0 of the others.
+__device__ __forceinline__ int64_t part_slot(const Split& s, int p) {
+  return static_cast<int64_t>(s.kf + p) * 2 + (p == 0 ? 1 : 0);
 }
 // Weight of a part with maximum m and sum l: a part without a row has l = 0, and its O is not
 // written; NaN scores leave l NaN, and perhaps m = -inf.
@@ -1081,119 +1116,131 @@ __device__ __forceinline__ void store_lse(const Args& a, int64_t out_row, bool a
   if (a.p.lse) a.p.lse[out_row] = any ? ref * 0.6931471805599453f + logf(den) : sink;
 }
 
+// A warp for two heads and 256 channels: lane i has head i % 2 and 4 of every 64 channels.
 __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_few_kernel(const Args a) {
   __shared__ Split sp;
   griddep_wait();  // the parts are complete
   if (threadIdx.x == 0) sp = split_of(a, blockIdx.x);
   __syncthreads();
-  const int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, q4 = lane >> 1;
+  const int row0 = (blockIdx.y * kJoinWarps + (threadIdx.x >> 5)) * 2, row = row0 + (lane & 1);
+  if (!sp.ok || sp.hg * kHeads + row0 >= a.p.H) return;
   const int head = sp.hg * kHeads + row;
-  if (!sp.ok || head >= a.p.H) return;
-  const int parts = sp.parts;  // at most kFewParts
+  const bool live = head < a.p.H;  // (an odd number of heads)
+  const int parts = sp.parts;      // at most kFewParts
   const int64_t out_row = sp.t * a.p.H + head;
-  const float sink = a.p.sink ? a.p.sink[head] : -INFINITY;
+  const float sink = a.p.sink && live ? a.p.sink[head] : -INFINITY;
+  // lane 2 p + (head % 2) has part p's m and l
   float2 ml = make_float2(-INFINITY, 0.f);
-  if (lane < parts) ml = a.part_ml[part_row(sp, lane, row)];
+  if (q4 < parts) ml = a.part_ml[part_slot(sp, q4) * kHeads + row];
   float M = ml.x;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  for (int o = 16; o > 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   M = fmaxf(M, sink * kLog2e);
   const float ref = M == -INFINITY ? 0.f : M;
   const float w = part_weight(ml, ref);
   float den = ml.y == 0.f ? 0.f : w * ml.y;
+  float any = ml.y == 0.f ? 0.f : 1.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+  for (int o = 16; o > 1; o >>= 1) {
+    den += __shfl_xor_sync(0xffffffffu, den, o);
+    any += __shfl_xor_sync(0xffffffffu, any, o);
+  }
   if (a.p.sink) den += ex2_ftz(sink * kLog2e - ref);
-  const bool any = __any_sync(0xffffffffu, ml.y != 0.f);
-  if (lane == 0) store_lse(a, out_row, any, sink, ref, den);
+  if (lane < 2 && live && blockIdx.z == 0) store_lse(a, out_row, any != 0.f, sink, ref, den);
   const float inv = den != 0.f ? 1.f / den : 0.f;
-  for (int c0 = 0; c0 < a.p.c; c0 += 512) {
-    float4 o[4];
+  const int quads = static_cast<int>(a.p.c) / 4, c0 = blockIdx.z * 64 + q4;
+  float4 o[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int q = 0; q < 4; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
-    for (int p = 0; p < parts; ++p) {
-      const float wp = __shfl_sync(0xffffffffu, w, p);
-      if (wp == 0.f) continue;  // nothing to add (and perhaps nothing written)
-      const float* src = a.part_o + part_row(sp, p, row) * a.p.c + c0 + lane * 4;
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (c0 + q * 128 + lane * 4 < a.p.c)
-          o[q] = fma4(*reinterpret_cast<const float4*>(src + q * 128), wp, o[q]);
-    }
+  for (int p = 0; p < parts; ++p) {
+    const float wp = __shfl_sync(0xffffffffu, w, 2 * p + (lane & 1));
+    const float4* src = a.part_o + part_slot(sp, p) * quads * kHeads + row;
+    float4 v[4];
+    // (a part of weight 0 adds nothing, and perhaps was not written)
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      if (c0 + q * 128 + lane * 4 < a.p.c) store4(a, out_row, c0 + q * 128 + lane * 4, o[q], inv);
+      v[q] = wp != 0.f && c0 + q * 16 < quads ? src[static_cast<int64_t>(c0 + q * 16) * kHeads]
+                                              : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) o[q] = fma4(v[q], wp, o[q]);
   }
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (live && c0 + q * 16 < quads) store4(a, out_row, (c0 + q * 16) * 4, o[q], inv);
 }
 
+// A block for two heads and 256 channels: thread i has head i % 2 and 4 channels.
 constexpr int kJoinGroups = 8;
 __global__ void __launch_bounds__(128 * kJoinGroups) attention_join_many_kernel(const Args a) {
   constexpr int G = kJoinGroups;
   __shared__ Split sp;
-  __shared__ float weight[kMaxParts], red[3][4 * G];
+  __shared__ float weight[2][kMaxParts], red[3][2][4 * G];
   __shared__ float4 sums[G - 1][128];
-  const int tid = threadIdx.x, row = blockIdx.y;
+  const int tid = threadIdx.x, odd = tid & 1;
   griddep_wait();  // the parts are complete
   if (tid == 0) sp = split_of(a, blockIdx.x);
   __syncthreads();
-  const int head = sp.hg * kHeads + row;
-  if (!sp.ok || head >= a.p.H) return;
+  const int row = blockIdx.y * 2 + odd, head = sp.hg * kHeads + row;
+  if (!sp.ok || head - odd >= a.p.H) return;
+  const bool live = head < a.p.H;
   const int parts = sp.parts;
   const int64_t out_row = sp.t * a.p.H + head;
-  const float sink = a.p.sink ? a.p.sink[head] : -INFINITY;
-  // every part's m and l at once (there are fewer parts than threads)
+  const float sink = a.p.sink && live ? a.p.sink[head] : -INFINITY;
+  // every part's m and l at once (there are fewer than half as many parts as threads)
   float2 ml = make_float2(-INFINITY, 0.f);
-  if (tid < parts) ml = a.part_ml[part_row(sp, tid, row)];
+  if (tid / 2 < parts) ml = a.part_ml[part_slot(sp, tid / 2) * kHeads + row];
   float M = ml.x;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if ((tid & 31) == 0) red[0][tid >> 5] = M;
+  for (int o = 16; o > 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if ((tid & 31) < 2) red[0][odd][tid >> 5] = M;
   __syncthreads();
   M = sink * kLog2e;
 #pragma unroll
-  for (int w = 0; w < 4 * G; ++w) M = fmaxf(M, red[0][w]);
+  for (int w = 0; w < 4 * G; ++w) M = fmaxf(M, red[0][odd][w]);
   const float ref = M == -INFINITY ? 0.f : M;
   const float wt = part_weight(ml, ref);
-  if (tid < parts) weight[tid] = wt;
+  if (tid / 2 < parts) weight[odd][tid / 2] = wt;
   float den = ml.y == 0.f ? 0.f : wt * ml.y;
   float any = ml.y == 0.f ? 0.f : 1.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = 16; o > 1; o >>= 1) {
     den += __shfl_xor_sync(0xffffffffu, den, o);
     any += __shfl_xor_sync(0xffffffffu, any, o);
   }
-  if ((tid & 31) == 0) {
-    red[1][tid >> 5] = den;
-    red[2][tid >> 5] = any;
+  if ((tid & 31) < 2) {
+    red[1][odd][tid >> 5] = den;
+    red[2][odd][tid >> 5] = any;
   }
   __syncthreads();
   den = a.p.sink ? ex2_ftz(sink * kLog2e - ref) : 0.f;
   any = 0.f;
 #pragma unroll
   for (int w = 0; w < 4 * G; ++w) {
-    den += red[1][w];
-    any += red[2][w];
+    den += red[1][odd][w];
+    any += red[2][odd][w];
   }
-  if (tid == 0) store_lse(a, out_row, any != 0.f, sink, ref, den);
+  if (tid < 2 && live && blockIdx.z == 0) store_lse(a, out_row, any != 0.f, sink, ref, den);
   const float inv = den != 0.f ? 1.f / den : 0.f;
   const int g = tid >> 7, lane = tid & 127;
-  const int ch = lane * 4;  // c is at most 512
+  const int quads = static_cast<int>(a.p.c) / 4, c4 = blockIdx.z * 64 + (lane >> 1);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (ch < a.p.c) {
-#pragma unroll 4
+  if (c4 < quads) {
+#pragma unroll 8
     for (int p = g; p < parts; p += G) {
-      const float w = weight[p];
-      if (w == 0.f) continue;
-      o = fma4(*reinterpret_cast<const float4*>(a.part_o + part_row(sp, p, row) * a.p.c + ch), w, o);
+      const float w = weight[odd][p];
+      const float4 v = w != 0.f ? a.part_o[(part_slot(sp, p) * quads + c4) * kHeads + row]
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+      o = fma4(v, w, o);
     }
   }
   if (g > 0) sums[g - 1][lane] = o;
   __syncthreads();
-  if (g == 0 && ch < a.p.c) {
+  if (g == 0 && live && c4 < quads) {
 #pragma unroll
     for (int i = 0; i < G - 1; ++i) o = fma4(sums[i][lane], 1.f, o);
-    store4(a, out_row, ch, o, inv);
+    store4(a, out_row, c4 * 4, o, inv);
   }
 }
 
@@ -1215,7 +1262,8 @@ Plan plan_of(int64_t T, int H, int64_t most, int max_ctas) {
   p.items = T * p.groups;
   p.tiles_per_item = most > 0 ? static_cast<int>(ceil_div(most, kRows)) : 1;
   p.units = p.items * p.tiles_per_item;
-  p.strided = p.items >= kStridedItems * max_ctas;
+  // (unit numbers are 32-bit)
+  p.strided = p.items >= kStridedItems * max_ctas || p.units > 0x7fffffff - 2 * kMaxCtas;
   if (p.strided) {
     p.ctas = max_ctas;
   } else {
@@ -1245,11 +1293,15 @@ kvc_status launch_attention(const AttentionProblem& p, cudaStream_t st) {
   if (sms < 1) return KVC_ERR_CUDA;
   const int64_t most = (p.idx ? p.k : p.max_visible) + (p.win_start ? p.max_win : 0);
   const Plan pl = plan_of(p.T, p.H, most, sms < kMaxCtas ? sms : kMaxCtas);
-  if (pl.items > 0x7fffffff) return KVC_ERR_UNSUPPORTED;
+  if (pl.items > 0x7fffffff - 2 * kMaxCtas) return KVC_ERR_UNSUPPORTED;
   Args a{};
   a.p = p;
-  a.items = pl.items;
-  a.units = pl.units;
+  a.items = static_cast<int>(pl.items);
+  if (!pl.strided) {
+    a.per_cta = static_cast<int>(pl.units / pl.ctas);
+    a.extra = static_cast<int>(pl.units % pl.ctas);
+  }
+  a.wide_out = reinterpret_cast<uintptr_t>(p.out) % 32 == 0 && p.c % 16 == 0 && p.r % 16 == 0;
   a.tiles_per_item = pl.tiles_per_item;
   a.groups = pl.groups;
   a.ctas = pl.ctas;
@@ -1258,7 +1310,7 @@ kvc_status launch_attention(const AttentionProblem& p, cudaStream_t st) {
   a.na = (a.cn + 63) / 64;
   a.nr = (p.r + 63) / 64;
   a.part_ml = static_cast<float2*>(p.workspace);
-  a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + ml_bytes(pl.ctas));
+  a.part_o = reinterpret_cast<float4*>(static_cast<uint8_t*>(p.workspace) + ml_bytes(pl.ctas));
   attention_kernel<<<pl.ctas, kThreads, kSmem, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return KVC_ERR_CUDA;
   const bool whole = pl.units % pl.ctas == 0 && (pl.units / pl.ctas) % pl.tiles_per_item == 0;
@@ -1274,7 +1326,8 @@ kvc_status launch_attention(const AttentionProblem& p, cudaStream_t st) {
     const bool few = parts <= kFewParts;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(splits),
-                       static_cast<unsigned>(few ? ceil_div(rows, kJoinWarps) : rows), 1);
+                       static_cast<unsigned>(few ? ceil_div(rows, 2 * kJoinWarps) : ceil_div(rows, 2)),
+                       static_cast<unsigned>(ceil_div(p.c, 256)));
     cfg.blockDim = dim3(few ? 32 * kJoinWarps : 128 * kJoinGroups, 1, 1);
     cfg.stream = st;
     cfg.attrs = attr;

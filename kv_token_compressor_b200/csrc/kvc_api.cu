@@ -23,10 +23,8 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 bool mul_ok(int64_t a, int64_t b, int64_t* r) { return !__builtin_mul_overflow(a, b, r); }
 
-// Device (or managed) memory of the current device.
-kvc_status check_device_ptr(const void* p) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return KVC_ERR_CUDA;
+// Device (or managed) memory of the current device `dev`.
+kvc_status check_device_ptr(const void* p, int dev) {
   cudaPointerAttributes at;
   if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
     cudaGetLastError();  // clear the error this query leaves for unknown pointers
@@ -38,12 +36,16 @@ kvc_status check_device_ptr(const void* p) {
 }
 
 kvc_status check_ptrs(const void* const* ps, int n) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return KVC_ERR_CUDA;
   for (int i = 0; i < n; ++i) {
-    kvc_status s = check_device_ptr(ps[i]);
+    kvc_status s = check_device_ptr(ps[i], dev);
     if (s != KVC_OK) return s;
   }
   return KVC_OK;
 }
+
+kvc_status check_device_ptr(const void* p) { return check_ptrs(&p, 1); }
 
 // Common shape checks of the streaming calls.  Sets *empty when nothing is to be done.
 kvc_status check_stream_shape(int64_t batch, int64_t n, int64_t c, int32_t m, bool* empty,

@@ -170,9 +170,11 @@ def _ptr(t):
 
 
 def _stream(stream):
-    torch = _torch()
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the current stream's handle without a Stream object (a third of a microsecond against
+        # three, in calls that take ten)
+        C = _torch()._C
+        return C._cuda_getCurrentRawStream(C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -180,7 +182,7 @@ def _out(out, shape, dtype, like):
     torch = _torch()
     if out is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
-    if tuple(out.shape) != tuple(shape) or out.dtype != dtype:
+    if out.shape != shape or out.dtype != dtype:
         raise ValueError(f"out must be {tuple(shape)} {dtype}")
     return out
 
@@ -333,7 +335,7 @@ def hca_compress_scalar_logits(C, z, b, m: int = 128, out=None, out_dtype=None, 
 
 def _index(t, num):
     torch = _torch()
-    if t.dtype != torch.int64 or tuple(t.shape) != (num,):
+    if t.dtype != torch.int64 or t.shape != (num,):
         raise ValueError("index arrays must be int64 [num]")
     return _ptr(t)
 
@@ -657,18 +659,24 @@ def partial_rope(x, pos, inv_freq, r: int, layout: str = "interleaved", inverse:
     int64 [T], inv_freq fp32 [r / 2]); inverse=True rotates back (also the gradient of the
     forward call).  out=x works in place.  Returns out."""
     torch = _torch()
-    if layout not in _ROPE_LAYOUTS:
+    code = _ROPE_LAYOUTS.get(layout)
+    if code is None:
         raise ValueError(f"layout must be one of {sorted(_ROPE_LAYOUTS)}, got {layout!r}")
     T, H, c = x.shape
-    code = _dtype_code(x.dtype)
-    out = _out(out, (T, H, c), x.dtype, x)
+    dtype = _dtype_code(x.dtype)
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    elif out is not x:
+        _out(out, (T, H, c), x.dtype, x)
     ppos = pfreq = None
     if r > 0:
         _need("inv_freq", inv_freq, r // 2, torch.float32)
         ppos, pfreq = _index(pos, T), _ptr(inv_freq)
-    st = lib().partial_rope(_ptr(x), _ptr(out), code, T, H, c, r, ppos, pfreq, _ROPE_LAYOUTS[layout],
-                            int(bool(inverse)), float(magnitude), _stream(stream))
-    _check(st, "partial_rope")
+    px = _ptr(x)
+    st = lib().partial_rope(px, px if out is x else _ptr(out), dtype, T, H, c, r, ppos, pfreq, code,
+                            1 if inverse else 0, magnitude, _stream(stream))
+    if st != KVC_OK:
+        raise KvcError(st, "partial_rope")
     return out
 
 
@@ -677,59 +685,74 @@ def shared_kv_attention_workspace_bytes(T: int, H: int, c: int, r: int, most_row
     return int(lib().shared_kv_attention_workspace_bytes(T, H, c, r, most_rows))
 
 
-def _cache_rows(nope, rope, c, r, what):
-    """Rows of a cache in the cache layout, after checking that both parts have them."""
+def _cache_ptrs(nope, rope, cn, r, what):
+    """(FP8 pointer, bf16 pointer, rows) of a cache in the cache layout, after checking that
+    both parts have them."""
     torch = _torch()
-    rows = None
-    if c - r > 0:
-        if nope is None or nope.dim() != 2 or nope.shape[1] != c - r or nope.dtype not in (
-                torch.uint8, torch.float8_e4m3fn):
-            raise ValueError(f"{what}nope must be E4M3 bytes [rows, {c - r}]")
+    pn = pr = None
+    rows = 0
+    if cn > 0:
+        if (nope is None or nope.dim() != 2 or nope.shape[1] != cn or
+                nope.dtype not in (torch.uint8, torch.float8_e4m3fn)):
+            raise ValueError(f"{what}nope must be E4M3 bytes [rows, {cn}]")
         rows = nope.shape[0]
+        pn = nope
     if r > 0:
         if rope is None or rope.dim() != 2 or rope.shape[1] != r or rope.dtype != torch.bfloat16:
             raise ValueError(f"{what}rope must be bf16 [rows, {r}]")
-        if rows is not None and rope.shape[0] != rows:
+        if cn > 0 and rope.shape[0] != rows:
             raise ValueError(f"{what}nope and {what}rope must have the same number of rows")
         rows = rope.shape[0]
-    return rows
+        pr = rope
+    return pn, pr, rows
 
 
-def _attention(name, q, nope, rope, key_start, n_visible, extra, most, r, scale, fp8_scale, window,
+def _attention(name, q, nope, rope, key_start, n_visible, idx, most, r, scale, fp8_scale, window,
                sink, out, want_lse, lse, workspace, stream):
     torch = _torch()
+    L = lib()
     T, H, c = q.shape
     _need("q", q, T * H * c, torch.bfloat16)
     cn = c - r
-    known = 0 <= r <= c  # else the library reports r
-    rows = _cache_rows(nope, rope, c, r, "") if known else 0
     wn = wr = ws = wl = None
-    wrows = max_win = 0
+    rows = wrows = max_win = 0
+    if 0 <= r <= c:  # else the library reports r
+        nope, rope, rows = _cache_ptrs(nope, rope, cn, r, "")
     if window is not None:
         wn, wr, ws, wl, max_win = window
-        wrows = _cache_rows(wn, wr, c, r, "window ") if known else 0
+        max_win = int(max_win)
+        if 0 <= r <= c:
+            wn, wr, wrows = _cache_ptrs(wn, wr, cn, r, "window ")
     if sink is not None:
         _need("sink", sink, H, torch.float32)
-    out = _out(out, (T, H, c), torch.bfloat16, q)
-    if want_lse or lse is not None:
-        lse = _out(lse, (T, H), torch.float32, q)
-    wargs = (_ptr(wn) if cn > 0 else None, _ptr(wr) if r > 0 else None, wrows,
-             _index(ws, T) if window is not None else None,
-             _index(wl, T) if window is not None else None, int(max_win))
-    nbytes = shared_kv_attention_workspace_bytes(T, H, c, r, most + int(max_win))
-    if workspace is None and nbytes > 0:
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        _out(out, (T, H, c), torch.bfloat16, q)
+    if lse is not None:
+        _out(lse, (T, H), torch.float32, q)
+    elif want_lse:
+        lse = q.new_empty((T, H), dtype=torch.float32)
+    ptrs = (_ptr(q), _ptr(nope), _ptr(rope), _index(key_start, T), _index(n_visible, T), _ptr(wn),
+            _ptr(wr), None if ws is None else _index(ws, T), None if wl is None else _index(wl, T))
+    nbytes = L.shared_kv_attention_workspace_bytes(T, H, c, r, most + max_win)
+    given = 0
+    if workspace is not None:
+        given = workspace.numel() * workspace.element_size()
+    elif nbytes > 0:
+        given = nbytes
         if stream is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            workspace = q.new_empty((nbytes,), dtype=torch.uint8)
         else:  # from the launching stream's pool: its reuse is ordered after the kernels
             with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=q.device)):
                 workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    st = getattr(lib(), name)(
-        _ptr(q), T, H, c, r, _ptr(nope) if cn > 0 else None, _ptr(rope) if r > 0 else None, rows,
-        float(fp8_scale), _index(key_start, T), _index(n_visible, T), *extra, *wargs, _ptr(sink),
-        float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
-        workspace.numel() * workspace.element_size() if workspace is not None else 0,
-        _stream(stream))
-    _check(st, name)
+    pq, pn, pr, pks, pnv, pwn, pwr, pws, pwl = ptrs
+    selected = (most,) if idx is None else (_ptr(idx), most)
+    st = getattr(L, name)(pq, T, H, c, r, pn, pr, rows, fp8_scale, pks, pnv, *selected, pwn, pwr,
+                          wrows, pws, pwl, max_win, _ptr(sink), scale, _ptr(out), _ptr(lse),
+                          _ptr(workspace), given, _stream(stream))
+    if st != KVC_OK:
+        raise KvcError(st, name)
     return out, lse
 
 
@@ -741,9 +764,9 @@ def shared_kv_attention(q, nope, rope, key_start, n_visible, max_visible: int, r
     value at once), with optional window rows (window = (win_nope, win_rope, win_start,
     win_len, max_win)) and per-head sink logits (fp32 [H]).  Returns (out [T, H, c] bf16,
     lse fp32 [T, H] or None)."""
-    return _attention("shared_kv_attention", q, nope, rope, key_start, n_visible,
-                      (int(max_visible),), int(max_visible), r, scale, fp8_scale, window, sink, out,
-                      want_lse, lse, workspace, stream)
+    return _attention("shared_kv_attention", q, nope, rope, key_start, n_visible, None,
+                      int(max_visible), r, scale, fp8_scale, window, sink, out, want_lse, lse,
+                      workspace, stream)
 
 
 def shared_kv_attention_topk(q, nope, rope, key_start, n_visible, idx, r: int, scale: float,
@@ -752,12 +775,10 @@ def shared_kv_attention_topk(q, nope, rope, key_start, n_visible, idx, r: int, s
     """shared_kv_attention over the listed entries idx [T, k] int32 (indexer_topk's output:
     indices within the query's visible entries, -1 for none) instead of all visible ones."""
     torch = _torch()
-    T = q.shape[0]
-    if idx.dtype != torch.int32 or idx.dim() != 2 or idx.shape[0] != T:
+    if idx.dtype != torch.int32 or idx.dim() != 2 or idx.shape[0] != q.shape[0]:
         raise ValueError("idx must be int32 [T, k]")
-    k = idx.shape[1]
-    return _attention("shared_kv_attention_topk", q, nope, rope, key_start, n_visible,
-                      (_ptr(idx), k), k, r, scale, fp8_scale, window, sink, out, want_lse, lse,
+    return _attention("shared_kv_attention_topk", q, nope, rope, key_start, n_visible, idx,
+                      idx.shape[1], r, scale, fp8_scale, window, sink, out, want_lse, lse,
                       workspace, stream)
 
 
