@@ -212,6 +212,32 @@ __device__ __forceinline__ void st_global32(void* p, const uint32_t (&v)[8]) {
                "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint2 lo, uint2 hi) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(lo.x), "r"(lo.y),
+               "r"(hi.x), "r"(hi.y)
+               : "memory");
+}
+__device__ __forceinline__ void st_shared4(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+// Larger magnitude (as 16-bit patterns: NaN above infinity above the rest) in either half.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t top, uint32_t w) {
+  return __vmaxu2(top, w & 0x7fff7fffu);
+}
+// A pair of bf16 values times a power of two, as fp16.
+__device__ __forceinline__ uint32_t scale_narrow(uint32_t w, float mul) {
+  const __half2 h =
+      __floats2half2_rn(__uint_as_float(w << 16) * mul, __uint_as_float(w & 0xffff0000u) * mul);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
 // 16 bytes from global to shared memory, asynchronously; zeros if not wanted.
 __device__ __forceinline__ void copy_chunk(uint32_t dst, const void* p, bool want) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p),
@@ -444,56 +470,53 @@ __device__ __forceinline__ void gather(const Args& a, const Shared& sh) {
     const int rr = pw * kOwn + rsub;
     if (rr < heads && lc * 64 < a.p.c) prefetch_l2(qb + rr * a.p.c + lc * 64);
   };
+  // Copied to its place as it is, then scaled and narrowed there: loops of a few instructions,
+  // since all of it runs once a segment, from cold.
   auto load_q = [&](int item, uint32_t seg) {
     int heads;
     const __nv_bfloat16* qb = q_rows(item, &heads);
     const int blocks = na + a.nr;
+    const int qc0 = rsub < blocks ? channel_of(a, lane * 8) : -1;
+    const int qc1 = rsub + 4 < blocks ? channel_of(a, 256 + lane * 8) : -1;
+    const uint32_t to = smem_u32(smem + kSmQ) + rsub * kAtom + pw * (kOwn * 128);
 #pragma unroll 1
-    for (int i0 = 0; i0 < kOwn; i0 += 2) {
-      uint4 v[2][2];
+    for (int i = 0; i < kOwn; ++i) {
+      const int rr = pw * kOwn + i;
+      const uint32_t at0 = to + i * 128 + ((lc ^ (rr & 7)) << 4);
+      const __nv_bfloat16* src = qb + rr * a.p.c;
+      const bool want0 = rr < heads && qc0 >= 0, want1 = rr < heads && qc1 >= 0;
+      if (rsub < blocks) copy_chunk(at0, want0 ? src + qc0 : a.p.q, want0);
+      if (rsub + 4 < blocks) copy_chunk(at0 + 4 * kAtom, want1 ? src + qc1 : a.p.q, want1);
+    }
+    copies_done();
+#pragma unroll 1
+    for (int i = 0; i < kOwn; ++i) {
+      const int rr = pw * kOwn + i;
+      const uint32_t at0 = to + i * 128 + ((lc ^ (rr & 7)) << 4);
+      uint4 v[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+      if (rsub < na) v[0] = ld_shared16(at0);
+      if (rsub + 4 < na) v[1] = ld_shared16(at0 + 4 * kAtom);
+      uint32_t top = 0;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int rr = pw * kOwn + i0 + i;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int qc = h * 4 + rsub < blocks ? channel_of(a, h * 256 + lane * 8) : -1;
-          v[i][h] = make_uint4(0u, 0u, 0u, 0u);
-          if (rr < heads && qc >= 0)
-            v[i][h] = __ldg(reinterpret_cast<const uint4*>(qb + rr * a.p.c + qc));
-        }
+      for (int h = 0; h < 2; ++h) {
+        top = max_abs_bf16x2(top, v[h].x);
+        top = max_abs_bf16x2(top, v[h].y);
+        top = max_abs_bf16x2(top, v[h].z);
+        top = max_abs_bf16x2(top, v[h].w);
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int rr = pw * kOwn + i0 + i;
-        uint32_t top = 0;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t w[4] = {v[i][h].x, v[i][h].y, v[i][h].z, v[i][h].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (h * 4 + rsub < na) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
-        }
-        int e = static_cast<int>(__reduce_max_sync(0xffffffffu, top) >> 7);
-        if (e == 255) e = 142;  // an infinity or NaN: no scaling
-        if (e < 16) e = 16;     // 2^(142 - e) stays finite
-        if (lane == 0) smem[kSmExp + (seg % kSegs) * kHeads + rr] = static_cast<uint8_t>(e);
-        const float mul = __int_as_float((142 - e + 127) << 23);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[4] = {v[i][h].x, v[i][h].y, v[i][h].z, v[i][h].w};
-          if (h * 4 + rsub < na) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const __half2 hh = __floats2half2_rn(__uint_as_float(w[k] << 16) * mul,
-                                                   __uint_as_float(w[k] & 0xffff0000u) * mul);
-              w[k] = *reinterpret_cast<const uint32_t*>(&hh);
-            }
-          }
-          if (h * 4 + rsub < blocks)
-            *reinterpret_cast<uint4*>(smem + kSmQ + (h * 4 + rsub) * kAtom + rr * 128 +
-                                      ((lc ^ (rr & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
+      top = max(top & 0xffffu, top >> 16);
+      int e = static_cast<int>(__reduce_max_sync(0xffffffffu, top) >> 7);
+      if (e == 255) e = 142;  // an infinity or NaN: no scaling
+      if (e < 16) e = 16;     // 2^(142 - e) stays finite
+      if (lane == 0) smem[kSmExp + (seg % kSegs) * kHeads + rr] = static_cast<uint8_t>(e);
+      const float mul = __int_as_float((142 - e + 127) << 23);
+      if (rsub < na)
+        st_shared16(at0, make_uint2(scale_narrow(v[0].x, mul), scale_narrow(v[0].y, mul)),
+                    make_uint2(scale_narrow(v[0].z, mul), scale_narrow(v[0].w, mul)));
+      if (rsub + 4 < na)
+        st_shared16(at0 + 4 * kAtom,
+                    make_uint2(scale_narrow(v[1].x, mul), scale_narrow(v[1].y, mul)),
+                    make_uint2(scale_narrow(v[1].z, mul), scale_narrow(v[1].w, mul)));
     }
   };
 
@@ -503,7 +526,6 @@ __device__ __forceinline__ void gather(const Args& a, const Shared& sh) {
   bool first = false, n_first = false;
   const int r = pw * kOwn + (lane & (kOwn - 1));
   cur.next(a, sh, r);
-  if (cur.item >= 0) prefetch_q(cur.item);
   while (true) {
     if (item >= 0) {
       const uint32_t st = gt % kStages;
@@ -987,6 +1009,31 @@ __device__ __forceinline__ void schedule(const Args& a, const Shared& sh) {
 
 // ------------------------------------------------------------------ the kernel
 
+// What the CTA's first segment needs, on its way into L2 while the CTA sets up: its query's row
+// range, its Q, the list entries of its first tiles.
+__device__ __forceinline__ void prefetch_first(const Args& a) {
+  const int u = a.strided ? blockIdx.x * a.tiles_per_item : first_unit(a, blockIdx.x);
+  const int item = u / a.tiles_per_item, tile = u - item * a.tiles_per_item;
+  const int64_t t = item / a.groups;
+  const int hg = item - static_cast<int>(t) * a.groups;
+  const int i = threadIdx.x;
+  if (i == 0) prefetch_l2(a.p.key_start + t);
+  if (i == 1) prefetch_l2(a.p.n_visible + t);
+  if (a.p.win_start) {
+    if (i == 2) prefetch_l2(a.p.win_start + t);
+    if (i == 3) prefetch_l2(a.p.win_len + t);
+  }
+  if (i >= 32 && i < 40 && a.p.idx) {
+    const int64_t e = static_cast<int64_t>(tile) * kRows + (i - 32) * 32;
+    if (e < a.p.k) prefetch_l2(a.p.idx + t * a.p.k + e);
+  }
+  // threads 64 .. : a row each 8, 64 channels a thread
+  const int row = (i - 64) >> 3, ch = (i & 7) * 64;
+  if (i >= 64 && row < kHeads && hg * kHeads + row < a.p.H && ch < a.p.c)
+    prefetch_l2(static_cast<const __nv_bfloat16*>(a.p.q) + (t * a.p.H + hg * kHeads + row) * a.p.c +
+                ch);
+}
+
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   griddep_launch_dependents();  // the join, which waits for this grid's end before it reads
@@ -994,6 +1041,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     if (threadIdx.x == 0) atomicOr(&g_attention_error, 1u);
     return;
   }
+  prefetch_first(a);
   Shared sh;
   sh.smem = smem;
   sh.bars = reinterpret_cast<uint64_t*>(smem + kSmBars);
@@ -1066,7 +1114,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 // it should be resident at once.  (A block for every head of every CTA boundary, most of
 // them idle, took 26 to 40 us.)
 constexpr int kMaxParts = 160;   // CTAs, with room
-constexpr int kFewParts = 8;
+constexpr int kFewParts = 16;   // two lanes for each
 constexpr int kJoinWarps = 4;
 
 struct Split {
