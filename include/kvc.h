@@ -388,6 +388,7 @@ typedef enum kvc_rope_layout {
  * also its gradient with respect to x.
  *   pos : [T] int64 device;  inv_freq : [r / 2] fp32 device;  magnitude : finite
  *   c % 8 == 0, r % 8 == 0, 0 <= r <= c, H >= 1;  x and out 16-byte aligned
+ *   r > 32768 or more than 2^30 16-byte units a token: KVC_ERR_UNSUPPORTED
  *   out == x works in place (only the last r channels are then touched); any other overlap
  *   of x and out returns KVC_ERR_POINTER.
  * The angle is formed and reduced modulo 2 pi in fp64, its sine and cosine and the rotation
@@ -435,7 +436,9 @@ KVC_API kvc_status kvc_rope_frequencies(int32_t r, double base, double factor, d
  *   bf16, not overlapping q;  lse [T, H] fp32 or NULL;  sink [H] fp32 or NULL (-inf: none)
  *   key_start, n_visible, win_start, win_len [T] int64;  idx [T, k] int32
  *   c % 8 == 0, r % 8 == 0, 0 <= r <= c and ceil((c - r) / 64) + ceil(r / 64) <= 8, else
- *   KVC_ERR_UNSUPPORTED;  H >= 1;  1 <= k <= 2^20;  fp8_scale finite and > 0;  scale finite
+ *   KVC_ERR_UNSUPPORTED;  H >= 1;  1 <= k <= 2^20;  fp8_scale finite and > 0;  scale finite;
+ *   most (below) <= 2^31 - 64, T ceil(H / 64) < 2^31 - 300, and 1 / fp8_scale and
+ *   scale / fp8_scale in fp32's range, else KVC_ERR_UNSUPPORTED
  *   q, nope, rope, out 16-byte aligned.
  * Checked on the device: a query whose n_visible is negative or (dense) above max_visible,
  *   whose win_len leaves [0, max_win], or one of whose groups leaves its arrays, is skipped

@@ -74,9 +74,12 @@ constexpr int kAtom = 64 * 128;   // one [64 rows or heads x 64] block of 16-bit
 constexpr int kStage = kMaxAtoms * kAtom;
 constexpr int kSegs = 4;          // segment records (and posted sums) under way
 // Bounded waits: polls before a wait gives up (each tens of cycles at least, so a few tenths of
-// a second; the longest wait of a sound run is microseconds).  Reading the nanosecond timer
-// between polls took thousands of cycles and made every wait that long.
+// a second; a sound run waits microseconds, except for the end of a segment, which may wait
+// kTilePolls more for each of its tiles).  Reading the nanosecond timer between polls took
+// thousands of cycles and made every wait that long.
 constexpr uint32_t kSpinLimit = 1u << 18;
+constexpr uint32_t kTilePolls = 1u << 9;
+constexpr int kTilesCounted = 1 << 22;  // (2^31 polls at most)
 constexpr long long kSchedLimit = 200000000000ll;  // cycles: a record may wait for long segments
 // Weights are exp2(x - m + kBias): with m at most kSlack below the running maximum they stay
 // below 2^15 in fp16 and vanish only 2^-31 below the maximum.
@@ -271,12 +274,13 @@ __device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity) {
 }
 // Bounded wait of a whole warp; one answer for its lanes.  (No function call: calls do not go
 // with setmaxnreg.)
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          uint32_t limit = kSpinLimit) {
 #pragma unroll 1
   for (uint32_t spins = 1;; ++spins) {
     if (__all_sync(0xffffffffu, try_wait_long(bar, parity))) return true;
     if (spins % 16 != 0) continue;
-    if (spins >= kSpinLimit) {
+    if (spins >= limit) {
       *abort_flag = 1;
       atomicOr(&g_attention_error, 1u);
     }
@@ -769,7 +773,8 @@ __device__ __forceinline__ void store_out_rows(const Args& a, const Shared& sh) 
     if (nt > 0) {
       g += nt;
       const uint32_t gl = g - 1;
-      if (!sh.wait(kBLFull + seg % kSegs, (seg / kSegs) & 1u) ||
+      if (!wait_warp(sh.bars + kBLFull + seg % kSegs, (seg / kSegs) & 1u, sh.abort_flag,
+                     kSpinLimit + kTilePolls * min(nt, kTilesCounted)) ||
           !sh.wait(kBPvDone + (gl & 1u), (gl >> 1) & 1u))
         return;
       tc_fence_after();
@@ -1012,8 +1017,13 @@ __device__ __forceinline__ void schedule(const Args& a, const Shared& sh) {
 // What the CTA's first segment needs, on its way into L2 while the CTA sets up: its query's row
 // range, its Q, the list entries of its first tiles.
 __device__ __forceinline__ void prefetch_first(const Args& a) {
-  const int u = a.strided ? blockIdx.x * a.tiles_per_item : first_unit(a, blockIdx.x);
-  const int item = u / a.tiles_per_item, tile = u - item * a.tiles_per_item;
+  int item = blockIdx.x, tile = 0;
+  if (!a.strided) {
+    const int u = first_unit(a, blockIdx.x);
+    item = u / a.tiles_per_item;
+    tile = u - item * a.tiles_per_item;
+  }
+  if (item >= a.items) return;
   const int64_t t = item / a.groups;
   const int hg = item - static_cast<int>(t) * a.groups;
   const int i = threadIdx.x;

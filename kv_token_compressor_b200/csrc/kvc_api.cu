@@ -159,6 +159,10 @@ kvc_status attention_call(const kvc::AttentionProblem& p, bool listed, int64_t w
   if (listed && (p.k < 1 || p.k > (int64_t(1) << 20))) return KVC_ERR_SHAPE;
   if (!std::isfinite(p.fp8_scale) || !(p.fp8_scale > 0.f) || !std::isfinite(p.scale))
     return KVC_ERR_SHAPE;
+  // the kernel multiplies by 1 / fp8_scale and by log2(e) scale / fp8_scale
+  if (!std::isfinite(1.f / p.fp8_scale) || !std::isfinite(1.45f * p.scale / p.fp8_scale) ||
+      !std::isfinite(1.45f * p.scale))
+    return KVC_ERR_UNSUPPORTED;
   int64_t t = 0;
   if (!mul_ok(p.cache_rows, p.c * 2, &t) || (win && !mul_ok(p.win_rows, p.c * 2, &t)) ||
       (listed && (!mul_ok(p.T, p.k, &t) || !mul_ok(t, 4, &t))))
@@ -166,7 +170,7 @@ kvc_status attention_call(const kvc::AttentionProblem& p, bool listed, int64_t w
   int64_t most = listed ? p.k : p.max_visible;
   if (win && __builtin_add_overflow(most, p.max_win, &most)) return KVC_ERR_SHAPE;
   if (p.T == 0) return KVC_OK;
-  if (most > (int64_t(1) << 31) - 1) return KVC_ERR_UNSUPPORTED;  // 32-bit row counts
+  if (most > (int64_t(1) << 31) - 64) return KVC_ERR_UNSUPPORTED;  // 32-bit row counts
   const bool rows = p.cache_rows > 0, wrows = win && p.win_rows > 0;
   if (!p.q || !p.out || !p.key_start || !p.n_visible || (listed && !p.idx)) return KVC_ERR_NULL;
   if ((rows && ((cn > 0 && !p.nope) || (r > 0 && !p.rope))) || (win && !p.win_len) ||
@@ -1011,6 +1015,7 @@ kvc_status partial_rope(const void* x, void* out, kvc_dtype dtype, int64_t T, in
   if (!mul_ok(T, H, &bytes) || !mul_ok(bytes, c, &bytes) ||
       !mul_ok(bytes, dtype == KVC_BF16 ? 2 : 4, &bytes))
     return KVC_ERR_SHAPE;
+  if (r > 32768) return KVC_ERR_UNSUPPORTED;  // a token's sines and cosines in shared memory
   if (T == 0 || c == 0 || (r == 0 && x == out)) return KVC_OK;
   if (!x || !out || (r > 0 && (!pos || !inv_freq))) return KVC_ERR_NULL;
   if (!aligned(x, 16) || !aligned(out, 16) || (r > 0 && (!aligned(pos, 8) || !aligned(inv_freq, 4))))

@@ -203,3 +203,17 @@ def test_binding_refuses_lists_and_rope_arguments(L):
         kvc.partial_rope(x, pos.int(), f, 32, out=x)  # int32 positions
     with pytest.raises(TypeError):
         kvc.partial_rope(x.double(), pos, f, 32)
+
+
+def test_limits_of_what_the_kernels_hold(L):
+    """Sizes and scales that would leave 32-bit counts, shared memory or fp32's range."""
+    assert rope(L, c=32776, r=32776, x=None) == kvc.KVC_ERR_UNSUPPORTED
+    assert rope(L, c=32776, r=32768, x=None) == kvc.KVC_ERR_NULL  # the shape is accepted
+    for topk in (False, True):
+        assert att(L, topk, s=1e-39) == kvc.KVC_ERR_UNSUPPORTED       # 1 / fp8_scale overflows
+        assert att(L, topk, s=1e-20, scale=1e19) == kvc.KVC_ERR_UNSUPPORTED
+        assert att(L, topk, scale=3e38) == kvc.KVC_ERR_UNSUPPORTED    # times log2(e)
+        assert att(L, topk, s=1e-38, scale=1e-3, q=None) == kvc.KVC_ERR_NULL
+    assert att(L, sel=((1 << 31) - 64,), mw=0, q=None) == kvc.KVC_ERR_NULL
+    assert att(L, sel=((1 << 31) - 63,), mw=0, q=None) == kvc.KVC_ERR_UNSUPPORTED
+    assert att(L, sel=((1 << 31) - 64,), mw=1, q=None) == kvc.KVC_ERR_UNSUPPORTED

@@ -544,3 +544,58 @@ def test_decode_step_together():
     got = back.double().cpu().numpy()
     lim = np.abs(out.double().cpu().numpy()).max()
     assert np.all(np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -20 * lim)
+
+
+@pytest.mark.parametrize("T,H,n", [(1, 130, 9000), (1, 7, 20000), (2, 65, 5000), (3, 1, 12000),
+                                   (40, 66, 500), (100, 128, 300), (149, 64, 190)])
+def test_split_queries_and_the_bounds_of_the_workspace(T, H, n):
+    """Queries in two to more than a hundred parts, odd heads, several head groups; a workspace
+    of exactly the stated bytes, full of NaN patterns, between guards."""
+    lens = [n - (t * 977) % n for t in range(T)]
+    p = Problem(T, H, 512, 64, [3] * T, lens, seed=T + H, sink=True,
+                window=([0] * T, [t % 9 for t in range(T)], 8))
+    need = kvc.shared_kv_attention_workspace_bytes(T, H, 512, 64, n + 8)
+    assert need > 0
+    buf = torch.full((need + 8192,), 0xFF, dtype=torch.uint8, device="cuda")
+    out, lse = p.run(workspace=buf[4096: 4096 + need])
+    assert kvc.device_status() == kvc.KVC_OK
+    p.check(out, lse, range(0, T, max(1, T // 8)))
+    assert bool(torch.all(buf[:4096] == 0xFF)) and bool(torch.all(buf[4096 + need:] == 0xFF))
+    again, lse2 = p.run(workspace=buf[4096: 4096 + need])
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("listed", [False, True])
+@pytest.mark.parametrize("T", [591, 592, 1300])
+def test_many_queries_on_both_sides_of_whole_query_scheduling(T, listed):
+    """Two head groups each: 1182, 1184 and 2600 items, the CTAs' ranges below 1184 and whole
+    items in turn from there; empty queries and windows among them, outputs between guards."""
+    rng = np.random.default_rng(T)
+    lens = [(t * 31) % 140 for t in range(T)]
+    idx = _lists(rng, lens, 70, holes=0.1) if listed else None
+    wl = [(t * 5) % 7 for t in range(T)]
+    p = Problem(T, 70, 128, 64, [(t * 3) % 40 for t in range(T)], lens, seed=T, idx=idx, sink=True,
+                window=([t for t in range(T)], wl, 6))
+    buf = torch.full((T * 70 * 128 + 4096,), 7.0, dtype=torch.bfloat16, device="cuda")
+    lbuf = torch.full((T * 70 + 512,), 7.0, device="cuda")
+    out, lse = buf[2048: -2048].view(T, 70, 128), lbuf[256: -256].view(T, 70)
+    p.run(out=out, lse=lse)
+    assert kvc.device_status() == kvc.KVC_OK
+    p.check(out, lse, [*range(0, T, 37), T - 1])
+    for g in (buf[:2048], buf[-2048:], lbuf[:256], lbuf[-256:]):
+        assert bool(torch.all(g == 7.0))
+
+
+def test_partial_rope_many_pairs():
+    """Up to 2^14 pairs a token, whose sines and cosines take 128 KB of shared memory."""
+    g = torch.Generator().manual_seed(5)
+    for c, r, half in ((32776, 32768, False), (16384, 16384, True), (4104, 4096, True)):
+        x = torch.randn((3, 2, c), generator=g)
+        pos, f = torch.tensor([0, 5, 70000]), kvc.rope_frequencies(r)
+        got = kvc.partial_rope(x.cuda(), pos.cuda(), f, r, layout="half" if half else "interleaved")
+        ref = AT.partial_rope(x.double().numpy(), pos.numpy(), f.double().cpu().numpy(), r, half)
+        # |a| + |b| <= 12 for these; each value within 2^-21 of it and its own rounding
+        assert float(x.abs().max()) <= 6
+        err = np.abs(got.double().cpu().numpy() - ref)
+        assert np.all(err <= 12 * 2.0 ** -21 + 2.0 ** -24 * np.abs(ref))
+    assert kvc.device_status() == kvc.KVC_OK
