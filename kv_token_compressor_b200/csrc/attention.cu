@@ -44,6 +44,8 @@ namespace kvc {
 
 // bit 0: a bounded wait gave up; bit 1: a query's rows or a listed entry out of range.
 __device__ unsigned int g_attention_error = 0;
+// What a row that does not count reads: E4M3 zeros.
+__device__ __align__(16) const uint8_t g_zero_row[512] = {};
 
 namespace attn {
 
@@ -51,7 +53,9 @@ using namespace tcx;
 
 // A segment of work, as the scheduler warp posts it in shared memory: tiles [j0, j1) of one
 // query's rows for one group of heads.  part: -1 the whole query, else this CTA's slot for the
-// partial result; t < 0 ends the list.
+// partial result; t < 0 ends the list.  Segments without a tile are not posted: the store
+// warps, which have their outputs to write, walk the CTA's units themselves.  (Posted, a run of
+// them longer than the ring would stop the roles that read ahead of the store.)
 struct Seg {
   int64_t t, key_start, win_start, n_visible;
   int hg, j0, j1, n1, n2, part, ok, item;
@@ -67,12 +71,13 @@ constexpr int kLoad0 = kSoftWarps + kStoreWarps;  // first gather warp
 constexpr int kMmaWarp = kLoad0 + kLoadWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 4);  // whole warpgroups for setmaxnreg
 // Registers a thread: 72 at launch (896 threads), 112 for the softmax.
-constexpr int kSoftRegs = 112, kStoreRegs = 56, kLoadRegs = 72, kMmaRegs = 48;
+constexpr int kSoftRegs = 104, kStoreRegs = 56, kLoadRegs = 72, kMmaRegs = 56;
 static_assert(kSoftRegs + kStoreRegs + 4 * kLoadRegs + kMmaRegs <= 7 * 72, "register split");
 constexpr int kMaxAtoms = 8;      // 64-channel blocks of a row
 constexpr int kAtom = 64 * 128;   // one [64 rows or heads x 64] block of 16-bit values, 8 KB
 constexpr int kStage = kMaxAtoms * kAtom;
-constexpr int kSegs = 4;          // segment records (and posted sums) under way
+constexpr int kSegs = 8;          // segment records under way
+constexpr int kExps = 4;          // and exponents of Q rows
 // Bounded waits: polls before a wait gives up (each tens of cycles at least, so a few tenths of
 // a second; a sound run waits microseconds, except for the end of a segment, which may wait
 // kTilePolls more for each of its tiles).  Reading the nanosecond timer between polls took
@@ -92,10 +97,11 @@ constexpr int kSmQ = 0;
 constexpr int kSmK = kSmQ + kMaxAtoms * kAtom;
 constexpr int kSmP = kSmK + kStages * kStage;        // [2][fp16, bf16] weights
 constexpr int kSmSeg = kSmP + 4 * kAtom;
-constexpr int kSmMl = kSmSeg + kSegs * int(sizeof(Seg));  // float2 [kSegs][kHeads] (m, l)
-constexpr int kSmExp = kSmMl + kSegs * kHeads * 8;   // u8 [kSegs][kHeads] exponents of Q rows
-constexpr int kSmMask = kSmExp + kSegs * kHeads;     // u8 [kStages][kLoadWarps]
-constexpr int kSmMisc = kSmMask + kStages * kLoadWarps;       // tmem address, abort flag
+constexpr int kSmRow = kSmSeg + kSegs * int(sizeof(Seg));  // u64 [2][kRows] where rows begin
+constexpr int kSmMl = kSmRow + 2 * kRows * 8;        // float2 [kHeads] (m, l)
+constexpr int kSmExp = kSmMl + kHeads * 8;           // u8 [kExps][kHeads] exponents of Q rows
+constexpr int kSmMask = kSmExp + kExps * kHeads;     // u32 [kStages][2] rows that count
+constexpr int kSmMisc = kSmMask + kStages * 8;       // tmem address, abort flag
 constexpr int kSmBars = kSmMisc + 8;
 // mbarriers, by index
 constexpr int kBKFull = 0;                  // [kStages] a row tile is in place
@@ -110,10 +116,12 @@ constexpr int kBOFree = kBPvDone + 2;       // O has been read (per segment)
 constexpr int kBLFull = kBOFree + 1;        // [kSegs] (m, l) posted
 constexpr int kBSegFull = kBLFull + kSegs;  // [kSegs] a segment record is posted
 constexpr int kBSegEmpty = kBSegFull + kSegs;  // [kSegs] every role has read it
-constexpr int kBFinal = kBSegEmpty + kSegs;
+constexpr int kBRowFull = kBSegEmpty + kSegs;  // [2] a tile's rows are known
+constexpr int kBRowEmpty = kBRowFull + 2;   // [2] their loads have set out
+constexpr int kBFinal = kBRowEmpty + 2;
 constexpr int kNumBars = kBFinal + 1;
 constexpr int kSmem = kSmBars + kNumBars * 8;
-static_assert(kSmBars % 8 == 0 && kSmMl % 8 == 0 && kSmMask % 16 == 0 && kOwn == 4, "layout");
+static_assert(kSmBars % 8 == 0 && kSmRow % 16 == 0 && kSmMask % 8 == 0 && kOwn == 4, "layout");
 static_assert(kSmem <= 227 * 1024, "attention shared memory");
 // TMEM columns: O 0-255; S buffer b 64 columns, S_n in the lower, S_r in the upper 16 lanes of
 // each quarter (as O's channels below and above 256).
@@ -160,6 +168,45 @@ __device__ __forceinline__ Query query_of(const AttentionProblem& a, int64_t t) 
          (n2 == 0 || (q.win_start >= 0 && q.win_start <= a.win_rows - n2));
   q.n1 = q.ok ? static_cast<int>(n1) : 0;
   q.n2 = q.ok ? static_cast<int>(n2) : 0;
+  return q;
+}
+
+// The CTA's units (items, if strided), and the next segment of them (t = -1 after the last).
+__device__ __forceinline__ void cta_range(const Args& a, int* at, int* end) {
+  const int cta = blockIdx.x;
+  *at = a.strided ? cta : first_unit(a, cta);
+  *end = a.strided ? a.items : first_unit(a, cta + 1);
+}
+__device__ __forceinline__ Seg next_segment(const Args& a, int* at, int end) {
+  Seg q;
+  q.t = -1;
+  q.j0 = q.j1 = 0;
+  if (*at >= end) return q;
+  const int tpi = a.tiles_per_item;
+  int item = *at, f0 = 0, f1 = tpi;
+  if (a.strided) {
+    *at += a.ctas;
+  } else {
+    item = *at / tpi;
+    f0 = *at - item * tpi;
+    if (end - *at < tpi - f0) f1 = f0 + end - *at;
+    *at += f1 - f0;
+  }
+  q.part = (f0 == 0 && f1 == tpi) ? -1 : (f0 > 0 ? 0 : 1);
+  q.item = item;
+  q.t = item / a.groups;
+  q.hg = item - static_cast<int>(q.t) * a.groups;
+  const Query y = query_of(a.p, q.t);
+  q.key_start = y.key_start;
+  q.win_start = y.win_start;
+  q.n_visible = y.n_visible;
+  q.n1 = y.n1;
+  q.n2 = y.n2;
+  q.ok = y.ok;
+  // a query shorter than the longest spreads its tiles over its CTAs alike
+  const int nt = (y.n1 + y.n2 + kRows - 1) / kRows;
+  q.j0 = f0 == 0 ? 0 : static_cast<int>(static_cast<int64_t>(f0) * nt / tpi);
+  q.j1 = f1 == tpi ? nt : static_cast<int>(static_cast<int64_t>(f1) * nt / tpi);
   return q;
 }
 
@@ -375,14 +422,14 @@ struct RowCursor {
   }
   // The row's number in its array (*win: the window's), -1 for one that does not count.  The
   // tile's segment record is still there: it is given back by the next() that leaves it.
-  __device__ __forceinline__ int64_t row(const Shared& sh, bool report, bool* win) {
+  __device__ __forceinline__ int64_t row(const Shared& sh, bool* win) {
     const Seg& q = sh.seg(sn - 1);
     *win = kind == 3;
     if (kind == 0) return -1;
     if (kind == 1) {
       raw = listed;
       if (raw < 0 || raw >= q.n_visible) {
-        if (raw != -1 && report) atomicOr(&g_attention_error, 2u);
+        if (raw != -1) atomicOr(&g_attention_error, 2u);
         return -1;
       }
     }
@@ -405,55 +452,39 @@ __device__ __forceinline__ void gather(const Args& a, const Shared& sh) {
   const int pw = (threadIdx.x >> 5) - kLoad0, lane = threadIdx.x & 31;
   const int lc = lane & 7, rsub = lane >> 3;
   const int na = a.na;
-  int off[2];        // channel of this lane's two chunks
-  uint32_t keep[2];  // 0: padding
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int ch = h * 256 + lane * 8;
-    keep[h] = ch < a.cn ? ~0u : 0u;
-    off[h] = ch < a.cn ? ch : 0;
-  }
-  RowCursor cur;
+  // channels of this lane's two chunks (of padding: others, which meet zeros of Q and are not
+  // stored to out)
+  const int off0 = lane * 8 < a.cn ? lane * 8 : 0;
+  const int off1 = 256 + lane * 8 < a.cn ? 256 + lane * 8 : 0;
   uint2 d[kOwn][2];
-  uint32_t bits = 0;  // which of the rows count
-  // lane i (mod 4): where row pw * 4 + i of the next tile begins (q, which is always there, for
-  // a row that does not count; what is read is dropped), and which of them count
-  const uint8_t *np = nullptr, *np_after = nullptr;
-  uint32_t nbits = 0, nbits_after = 0;
-  auto resolve = [&]() {  // ... of the tile after the next
-    bool win;
-    const int64_t row = cur.row(sh, lane < kOwn, &win);
-    nbits_after = __ballot_sync(0xffffffffu, row >= 0) & ((1u << kOwn) - 1u);
-    np_after = static_cast<const uint8_t*>(row < 0 ? a.p.q : win ? a.p.win_nope : a.p.nope);
-    if (row >= 0) np_after += row * a.cn;
-    // lanes 0-3 one 128-byte line of their row, lanes 4-7 the next, ...
-    if (row >= 0 && (lane >> 2) * 128 < a.cn) prefetch_l2(np_after + (lane >> 2) * 128);
-  };
-  auto load = [&]() {
-    bits = nbits;
+  auto load = [&](uint32_t gt) {
+    if (!sh.wait(kBRowFull + (gt & 1u), (gt >> 1) & 1u)) return false;
     if (na > 0) {
+      const ulonglong2* rows =
+          reinterpret_cast<const ulonglong2*>(smem + kSmRow + (gt & 1u) * (kRows * 8)) + pw * 2;
+      const ulonglong2 r01 = rows[0], r23 = rows[1];
+      const uint8_t* p[kOwn] = {
+          reinterpret_cast<const uint8_t*>(r01.x), reinterpret_cast<const uint8_t*>(r01.y),
+          reinterpret_cast<const uint8_t*>(r23.x), reinterpret_cast<const uint8_t*>(r23.y)};
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) {
-        const uint8_t* p = reinterpret_cast<const uint8_t*>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(np), i));
-        d[i][0] = ld_chunk(p + off[0]);
-        d[i][1] = ld_chunk(p + off[1]);
+        d[i][0] = ld_chunk(p[i] + off0);
+        d[i][1] = ld_chunk(p[i] + off1);
       }
     }
+    sh.arrive(kBRowEmpty + (gt & 1u));
+    return true;
   };
   auto store = [&](uint32_t st) {
     uint8_t* kb = smem + kSmK + st * kStage + rsub * kAtom;
-    if (lane == 0) smem[kSmMask + st * kLoadWarps + pw] = static_cast<uint8_t>(bits);
     if (na > 0) {
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) {
         const int rr = pw * kOwn + i;
         uint8_t* place = kb + rr * 128 + ((lc ^ (rr & 7)) << 4);
-        const uint32_t live = 0u - ((bits >> i) & 1u);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint2 lo = widen4(d[i][h].x & live & keep[h]);
-          const uint2 hi = widen4(d[i][h].y & live & keep[h]);
+          const uint2 lo = widen4(d[i][h].x), hi = widen4(d[i][h].y);
           if (h * 4 + rsub < na)
             *reinterpret_cast<uint4*>(place + h * 4 * kAtom) = make_uint4(lo.x, lo.y, hi.x, hi.y);
         }
@@ -466,13 +497,6 @@ __device__ __forceinline__ void gather(const Args& a, const Shared& sh) {
     *heads = a.p.H - hg * kHeads;
     return static_cast<const __nv_bfloat16*>(a.p.q) +
            (static_cast<int64_t>(t) * a.p.H + hg * kHeads) * a.p.c;
-  };
-  // A line of 64 channels for every lane: this warp's 4 rows are in L2 when their turn comes.
-  auto prefetch_q = [&](int item) {
-    int heads;
-    const __nv_bfloat16* qb = q_rows(item, &heads);
-    const int rr = pw * kOwn + rsub;
-    if (rr < heads && lc * 64 < a.p.c) prefetch_l2(qb + rr * a.p.c + lc * 64);
   };
   // Copied to its place as it is, then scaled and narrowed there: loops of a few instructions,
   // since all of it runs once a segment, from cold.
@@ -512,7 +536,7 @@ __device__ __forceinline__ void gather(const Args& a, const Shared& sh) {
       int e = static_cast<int>(__reduce_max_sync(0xffffffffu, top) >> 7);
       if (e == 255) e = 142;  // an infinity or NaN: no scaling
       if (e < 16) e = 16;     // 2^(142 - e) stays finite
-      if (lane == 0) smem[kSmExp + (seg % kSegs) * kHeads + rr] = static_cast<uint8_t>(e);
+      if (lane == 0) smem[kSmExp + (seg % kExps) * kHeads + rr] = static_cast<uint8_t>(e);
       const float mul = __int_as_float((142 - e + 127) << 23);
       if (rsub < na)
         st_shared16(at0, make_uint2(scale_narrow(v[0].x, mul), scale_narrow(v[0].y, mul)),
@@ -524,16 +548,19 @@ __device__ __forceinline__ void gather(const Args& a, const Shared& sh) {
     }
   };
 
-  uint32_t gt = 0, seg = 0;
-  int item = -1;       // of the tile whose loads are under way
-  int n_item = -1;     // of the tile whose rows are known
-  bool first = false, n_first = false;
-  const int r = pw * kOwn + (lane & (kOwn - 1));
-  cur.next(a, sh, r);
+  uint32_t gt = 0, sn = 0, seg = 0;
   while (true) {
-    if (item >= 0) {
+    if (!sh.wait(kBSegFull + sn % kSegs, (sn / kSegs) & 1u)) return;
+    const Seg& q = sh.seg(sn);
+    const int nt = q.j1 - q.j0, item = q.item;
+    const bool end = q.t < 0;
+    sh.arrive(kBSegEmpty + sn % kSegs);
+    if (end) return;
+    ++sn;
+    for (int i = 0; i < nt; ++i, ++gt) {
       const uint32_t st = gt % kStages;
-      if (first) {
+      if (!load(gt)) return;
+      if (i == 0) {
         if (!sh.wait(kBQEmpty, (seg & 1u) ^ 1u)) return;
         load_q(item, seg);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -544,64 +571,85 @@ __device__ __forceinline__ void gather(const Args& a, const Shared& sh) {
       store(st);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       sh.arrive(kBKFull + st);
-      ++gt;
-    }
-    item = n_item;
-    first = n_first;
-    n_item = cur.item;
-    n_first = cur.first;
-    if (item < 0 && n_item < 0) return;
-    // a listed row's number, on its way since the last turn, is needed before the loads set
-    // out: the wait for it would be one for them too
-    if (n_item >= 0) resolve();
-    if (item >= 0) load();
-    np = np_after;
-    nbits = nbits_after;
-    if (n_item >= 0) {
-      cur.next(a, sh, r);
-      if (cur.first && cur.item >= 0) prefetch_q(cur.item);
     }
   }
 }
 
 // ------------------------------------------------------------------ bf16 copy (2 warps)
 
-// The rows' bf16 channels go to their place as they are: a lane copies one row of a tile, 16
-// bytes at a time, once the place is free, after a prefetch into L2 one tile ahead.
-__device__ __forceinline__ void copy_bf16(const Args& a, const Shared& sh) {
+// A line of 64 channels after another of Q's row r: in L2 when its turn comes.
+__device__ __forceinline__ void prefetch_q(const Args& a, int item, int r) {
+  const int t = item / a.groups, head = (item - t * a.groups) * kHeads + r;
+  if (head >= a.p.H) return;
+  const __nv_bfloat16* q =
+      static_cast<const __nv_bfloat16*>(a.p.q) + (static_cast<int64_t>(t) * a.p.H + head) * a.p.c;
+#pragma unroll 1
+  for (int c = 0; c < a.p.c; c += 64) prefetch_l2(q + c);
+}
+
+// Where a tile's rows begin, for the gather, two tiles ahead of it and with a prefetch into L2;
+// and the rows' bf16 channels, which go to their place as they are.  A lane has one row of
+// every tile and copies it, 16 bytes at a time, once the place is free.
+__device__ __forceinline__ void copy_rows(const Args& a, const Shared& sh) {
   const int r = threadIdx.x & 63;  // (the two warps begin at a multiple of 64 threads)
   const int nr = a.nr;
   RowCursor cur;
-  uint32_t gt = 0;
+  uint32_t known = 0, ahead = 0;  // tiles whose rows have been handed on; looked for
+  // the row's bf16 channels in the next tiles to copy (nullptr: it does not count)
+  const __nv_bfloat16 *s0 = nullptr, *s1 = nullptr, *s2 = nullptr;
   cur.next(a, sh, r);
-  while (cur.item >= 0) {
-    bool win;
-    const int64_t row = cur.row(sh, false, &win);
-    const bool live = row >= 0;
-    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(
-        !live ? a.p.q : win ? a.p.win_rope : a.p.rope);
-    if (live) {
-      src += row * a.p.r;
-      for (int ch = 0; ch < a.p.r; ch += 64) prefetch_l2(src + ch);
+  for (uint32_t gt = 0;; ++gt) {
+#pragma unroll 1
+    while (true) {
+      s2 = nullptr;
+      if (cur.item >= 0) {
+        if (cur.first) prefetch_q(a, cur.item, r);
+        bool win;
+        const int64_t row = cur.row(sh, &win);
+        const uint8_t* nope = g_zero_row;
+        if (row >= 0) {
+          if (a.cn > 0) {
+            nope = static_cast<const uint8_t*>(win ? a.p.win_nope : a.p.nope) + row * a.cn;
+#pragma unroll 1
+            for (int c = 0; c < a.cn; c += 128) prefetch_l2(nope + c);
+          }
+          s2 = static_cast<const __nv_bfloat16*>(nr == 0 ? a.p.q
+                                                         : win ? a.p.win_rope : a.p.rope) +
+               row * a.p.r;
+#pragma unroll 1
+          for (int c = 0; c < a.p.r; c += 64) prefetch_l2(s2 + c);
+        }
+        const uint32_t b = known & 1u;
+        if (!sh.wait(kBRowEmpty + b, ((known >> 1) & 1u) ^ 1u)) return;
+        reinterpret_cast<const uint8_t**>(sh.smem + kSmRow)[b * kRows + r] = nope;
+        sh.arrive(kBRowFull + b);
+        ++known;
+        cur.next(a, sh, r);
+      }
+      if (++ahead == gt + 3) break;
+      s0 = s1;
+      s1 = s2;
     }
-    cur.next(a, sh, r);
+    if (gt == known) return;
     const uint32_t st = gt % kStages;
     if (!sh.wait(kBKEmpty + st, ((gt / kStages) & 1u) ^ 1u)) return;
-    const uint32_t dst =
-        smem_u32(sh.smem + kSmK + st * kStage + a.na * kAtom) + r * 128;
+    const uint32_t live = __ballot_sync(0xffffffffu, s0 != nullptr);
+    if ((r & 31) == 0) reinterpret_cast<uint32_t*>(sh.smem + kSmMask)[st * 2 + (r >> 5)] = live;
+    const uint32_t dst = smem_u32(sh.smem + kSmK + st * kStage + a.na * kAtom) + r * 128;
 #pragma unroll 1
     for (int k = 0; k < nr; ++k) {
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const bool want = live && k * 64 + c * 8 < a.p.r;
-        copy_chunk(dst + k * kAtom + ((c ^ (r & 7)) << 4), want ? src + k * 64 + c * 8 : a.p.q,
+        const bool want = s0 != nullptr && k * 64 + c * 8 < a.p.r;
+        copy_chunk(dst + k * kAtom + ((c ^ (r & 7)) << 4), want ? s0 + k * 64 + c * 8 : a.p.q,
                    want);
       }
     }
     copies_done();
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     sh.arrive(kBKFull + st);
-    ++gt;
+    s0 = s1;
+    s1 = s2;
   }
 }
 
@@ -626,7 +674,6 @@ __device__ __forceinline__ void softmax(const Args& a, const Shared& sh) {
     const int nt = q.j1 - q.j0;
     sh.arrive(kBSegEmpty + sn % kSegs);
     if (end) return;
-    if (nt == 0) continue;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, scale_n[2] = {0.f, 0.f};
 #pragma unroll 1
     for (int i = 0; i < nt; ++i, ++g) {
@@ -639,11 +686,11 @@ __device__ __forceinline__ void softmax(const Args& a, const Shared& sh) {
         // x = S_n * (2^(E - 142) scale / fp8_scale) + S_r * scale, in units of log 2
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const int e = smem[kSmExp + (seg % kSegs) * kHeads + ra + 8 * r];
+          const int e = smem[kSmExp + (seg % kExps) * kHeads + ra + 8 * r];
           scale_n[r] = n_scale * __int_as_float((e - 15) << 23);
         }
       }
-      const uint4 live = *reinterpret_cast<const uint4*>(smem + kSmMask + st * kLoadWarps);
+      const uint2 live = *reinterpret_cast<const uint2*>(smem + kSmMask + st * 8);
       float x[32];
       const uint32_t sb = lane_addr + kColS + 64 * b;
       float2 (&x2)[16] = *reinterpret_cast<float2(*)[16]>(x);  // [2 k + row]: two columns
@@ -671,11 +718,10 @@ __device__ __forceinline__ void softmax(const Args& a, const Shared& sh) {
       }
       tc_fence_before();
       sh.arrive(kBSFree + b);
-      if ((live.x & live.y & live.z & live.w) != 0x0f0f0f0fu) {  // 4 rows a byte
+      if ((live.x & live.y) != ~0u) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const uint32_t word = k < 2 ? live.x : k < 4 ? live.y : k < 6 ? live.z : live.w;
-          const uint32_t two = word >> (16 * (k & 1) + 8 * (q4 >> 1) + 2 * (q4 & 1));
+          const uint32_t two = (k < 4 ? live.x : live.y) >> (8 * (k & 3) + 2 * q4);
           if (!(two & 1u)) x[4 * k] = x[4 * k + 2] = -INFINITY;
           if (!(two & 2u)) x[4 * k + 1] = x[4 * k + 3] = -INFINITY;
         }
@@ -737,7 +783,9 @@ __device__ __forceinline__ void softmax(const Args& a, const Shared& sh) {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       sh.arrive(kBPFull + b);
     }
-    float2* ml = reinterpret_cast<float2*>(smem + kSmMl) + (seg % kSegs) * kHeads;
+    // the sums of the segment before this one have been read
+    if (seg > 0 && !sh.wait(kBOFree, (seg - 1) & 1u)) return;
+    float2* ml = reinterpret_cast<float2*>(smem + kSmMl);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -760,13 +808,13 @@ __device__ __forceinline__ void store_out_rows(const Args& a, const Shared& sh) 
   const int slots = (a.na + a.nr) * 64;
   const float inv_fp8 = 1.f / a.p.fp8_scale;
   uint32_t g = 0, seg = 0;
-  for (uint32_t sn = 0;; ++sn) {
-    if (!sh.wait(kBSegFull + sn % kSegs, (sn / kSegs) & 1u)) return;
-    const Seg& q = sh.seg(sn);
+  int at, end;
+  cta_range(a, &at, &end);
+  while (true) {
+    const Seg q = next_segment(a, &at, end);
     const int64_t t = q.t;
     const int nt = q.j1 - q.j0, hg = q.hg, part = q.part;
     const bool ok = q.ok;
-    sh.arrive(kBSegEmpty + sn % kSegs);
     if (t < 0) return;
     if (!ok && w == 0 && lane == 0) atomicOr(&g_attention_error, 2u);
     float m = -INFINITY, l = 0.f;
@@ -779,7 +827,7 @@ __device__ __forceinline__ void store_out_rows(const Args& a, const Shared& sh) 
         return;
       tc_fence_after();
       const float2 ml =
-          reinterpret_cast<const float2*>(sh.smem + kSmMl)[(seg % kSegs) * kHeads + row];
+          reinterpret_cast<const float2*>(sh.smem + kSmMl)[row];
       m = ml.x;
       l = ml.y;
       ++seg;
@@ -964,40 +1012,13 @@ __device__ __forceinline__ void issue_mmas(const Args& a, const Shared& sh) {
 
 __device__ __forceinline__ void schedule(const Args& a, const Shared& sh) {
   Seg* segs = reinterpret_cast<Seg*>(sh.smem + kSmSeg);
-  const int cta = blockIdx.x;
-  int at = a.strided ? cta : first_unit(a, cta);
-  const int end = a.strided ? a.items : first_unit(a, cta + 1);
-  const int tpi = a.tiles_per_item;
+  int at, end;
+  cta_range(a, &at, &end);
   for (uint32_t sn = 0;; ++sn) {
     Seg q;
-    q.t = -1;
-    q.j0 = q.j1 = 0;
-    if (at < end) {
-      int item = at, f0 = 0, f1 = tpi;
-      if (a.strided) {
-        at += a.ctas;
-      } else {
-        item = at / tpi;
-        f0 = at - item * tpi;
-        if (end - at < tpi - f0) f1 = f0 + end - at;
-        at += f1 - f0;
-      }
-      q.part = (f0 == 0 && f1 == tpi) ? -1 : (f0 > 0 ? 0 : 1);
-      q.item = item;
-      q.t = item / a.groups;
-      q.hg = item - static_cast<int>(q.t) * a.groups;
-      const Query y = query_of(a.p, q.t);
-      q.key_start = y.key_start;
-      q.win_start = y.win_start;
-      q.n_visible = y.n_visible;
-      q.n1 = y.n1;
-      q.n2 = y.n2;
-      q.ok = y.ok;
-      // a query shorter than the longest spreads its tiles over its CTAs alike
-      const int nt = (y.n1 + y.n2 + kRows - 1) / kRows;
-      q.j0 = f0 == 0 ? 0 : static_cast<int>(static_cast<int64_t>(f0) * nt / tpi);
-      q.j1 = f1 == tpi ? nt : static_cast<int>(static_cast<int64_t>(f1) * nt / tpi);
-    }
+    do {
+      q = next_segment(a, &at, end);
+    } while (q.t >= 0 && q.j0 == q.j1);
     const long long t0 = clock64();
     while (!mbar_try_wait(sh.bars + kBSegEmpty + sn % kSegs, ((sn / kSegs) & 1u) ^ 1u)) {
       if (clock64() - t0 > kSchedLimit) {
@@ -1067,7 +1088,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       if (i >= kBPFull && i < kBPFull + 2) count = kSoftWarps;
       if (i == kBOFree) count = kStoreWarps;
       if (i >= kBLFull && i < kBLFull + kSegs) count = kSoftWarps;
-      if (i >= kBSegEmpty && i < kBSegEmpty + kSegs) count = kMmaWarp + 3;
+      if (i >= kBSegEmpty && i < kBSegEmpty + kSegs) count = kMmaWarp + 3 - kStoreWarps;
+      if (i >= kBRowFull && i < kBRowFull + 2) count = 2;
+      if (i >= kBRowEmpty && i < kBRowEmpty + 2) count = kLoadWarps;
       mbar_init(sh.bars + i, count);
     }
     *sh.abort_flag = 0;
@@ -1101,7 +1124,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     } else if (warp == kMmaWarp + 1) {
       if (elect_one()) schedule(a, sh);
     } else {
-      copy_bf16(a, sh);
+      copy_rows(a, sh);
     }
   }
 

@@ -599,3 +599,19 @@ def test_partial_rope_many_pairs():
         err = np.abs(got.double().cpu().numpy() - ref)
         assert np.all(err <= 12 * 2.0 ** -21 + 2.0 ** -24 * np.abs(ref))
     assert kvc.device_status() == kvc.KVC_OK
+
+
+@pytest.mark.parametrize("T,every,most", [(3000, 400, 100), (3000, 2999, 200), (1000, 7, 1),
+                                          (1100, 60, 500), (2000, 5000, 64)])
+def test_long_runs_of_empty_queries(T, every, most):
+    """Padded batches: hundreds of queries without rows between those that have some, and at
+    the end."""
+    lens = [1 + (t * 17) % most if t % every == 0 else 0 for t in range(T)]
+    p = Problem(T, 20, 64, 64, [0] * T, lens, seed=T + every, sink=True)
+    out, lse = p.run(max_visible=most)
+    assert kvc.device_status() == kvc.KVC_OK
+    used = [t for t in range(T) if lens[t]]
+    p.check(out, lse, [*used, *range(1, T, 97)])
+    empty = torch.tensor([n == 0 for n in lens], device="cuda")
+    assert torch.count_nonzero(out[empty]).item() == 0
+    assert torch.equal(lse[empty], p.sink.cuda().expand(int(empty.sum()), 20))
