@@ -15,11 +15,18 @@
 // SM's TMEM (channels 0-255 in the lower 16 lanes of each quarter, 256-511 in the upper 16),
 // S double-buffered in the other half, and a tile of 64 rows is held once in shared memory as
 // the B operand of both GEMMs (K-major for S, MN-major for P K).  An M = 64 MMA takes as long
-// as one with M = 128 (measured: 32 cycles at N = 64, 128 at N = 256), so a tile costs 2060
-// tensor cycles.  Measured against it: two CTAs per query with 128 heads and half of the
-// channels each halve that on paper, but the half-sums of S they must exchange cross the
-// SM-to-SM network at 20 bytes a cycle and its latency (about 4000 cycles) sits in every
-// tile's chain: 5300 cycles a tile.
+// as one with M = 128 of the same N from N = 128 on (measured: 32 cycles at N = 64, 128 at
+// N = 256), so a tile costs 2060 tensor cycles, twice its share of the peak.  128 heads a CTA
+// would need all of TMEM for O alone.  Measured against it: two CTAs per query with 128 heads
+// and half of the channels each halve the MMA time on paper, but the half-sums of S they must
+// exchange cross the SM-to-SM network at 20 bytes a cycle and its latency (about 4000 cycles)
+// sits in every tile's chain: 5300 cycles a tile.
+//
+// What a tile takes: 4300 cycles (chunk of 1024 queries x 1152 rows x 128 heads: 580 us, 525
+// TFLOP/s).  With every load, conversion, exponential and store taken out 3100 remain, and the
+// hand-overs alone (no MMAs either) take 1000: S of a tile, its softmax, P K and the refill of
+// its place follow one another, two tiles in turn, and S reads Q and K from shared memory at
+// nearly all the bytes a cycle that it has, so that everything beside it waits.
 //
 // Types.  An E4M3 byte is exact in fp16, and a bf16 query row is exact in fp16 once scaled by
 // a power of two (its largest value to 2^15: what is lost lies 2^-40 below it), so the FP8
@@ -28,9 +35,10 @@
 // accumulators of their own (S_n, S_r), because only S_n carries the row's power of two and
 // 1 / fp8_scale.  Both parts accumulate in fp32.
 //
-// Roles.  Warps 0-3 take the softmax, 4-7 store finished queries, 8-23 gather the rows (FP8:
-// global memory -> registers -> widened, swizzled shared memory; 26-27 copy the bf16 channels),
-// warp 24 issues the MMAs, warp 25 walks the segments (query, row tiles) of its CTA and posts them to the others.  A query's
+// Roles of the 28 warps.  0-3 take the softmax, 4-7 store finished queries, 8-23 gather the
+// rows' FP8 channels (global memory -> registers -> widened, swizzled shared memory), 24
+// issues the MMAs, 25 walks the segments (query, row tiles) of its CTA and posts them to the
+// others, 26-27 find each tile's rows, tell the gather and copy the bf16 channels.  A query's
 // tiles are split among CTAs when there are too few queries, and a second kernel joins the
 // parts in a fixed order.
 #include <cuda_fp16.h>
@@ -70,7 +78,8 @@ constexpr int kOwn = kRows / kLoadWarps;          // rows of a tile per gather w
 constexpr int kLoad0 = kSoftWarps + kStoreWarps;  // first gather warp
 constexpr int kMmaWarp = kLoad0 + kLoadWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 4);  // whole warpgroups for setmaxnreg
-// Registers a thread: 72 at launch (896 threads), 112 for the softmax.
+// Registers a thread: 72 at launch (896 threads); the split is the least without spills, and
+// what is left goes to the softmax.
 constexpr int kSoftRegs = 104, kStoreRegs = 56, kLoadRegs = 72, kMmaRegs = 56;
 static_assert(kSoftRegs + kStoreRegs + 4 * kLoadRegs + kMmaRegs <= 7 * 72, "register split");
 constexpr int kMaxAtoms = 8;      // 64-channel blocks of a row
@@ -132,7 +141,7 @@ struct Args {
   AttentionProblem p;
   int items, tiles_per_item;  // an item: a query and a group of heads
   int groups, ctas;
-  int per_cta, extra;       // units (items x tiles_per_item): per CTA, one more for the first `extra`
+  int per_cta, extra;       // units (items x tiles_per_item) per CTA, one more in the first `extra`
   int na, nr;               // 64-channel blocks: FP8, then bf16
   int cn;                   // FP8 channels
   bool strided;             // whole items, CTA by CTA (no splits)
@@ -212,8 +221,8 @@ __device__ __forceinline__ Seg next_segment(const Args& a, int* at, int end) {
 
 // ------------------------------------------------------------------ PTX
 
-// TMEM <-> registers: 16 columns of a lane each (also tmem_ld16); tmem_ld_rows: 16 lanes x 64 columns, lane i
-// holding of rows i / 4 (v[4k], v[4k + 1]) and i / 4 + 8 (v[4k + 2], v[4k + 3]) the columns
+// TMEM <-> registers: 16 columns of a lane each (also tmem_ld16); tmem_ld_rows: 16 lanes x 64
+// columns, lane i holding of rows i / 4 (v[4k], v[4k + 1]) and i / 4 + 8 (v[4k + 2], v[4k + 3]) the columns
 // 8k + 2 (i % 4) and the next.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
   asm volatile(
@@ -443,10 +452,10 @@ struct RowCursor {
 // the MMAs read them: 128-byte rows of 64 16-bit channels, swizzled, widened to fp16.  Warp pw
 // has rows [4 pw, 4 pw + 4) of a tile, a lane the 8-channel chunks lane and lane + 32 of each
 // (a warp reads 256 consecutive bytes).  A tile's loads set out as soon as the registers of the
-// tile before are stored; its rows are prefetched into L2 one tile earlier.  (8 warps with 8
-// rows each took twice as long over a tile: the gather is bound by the latency of its
-// instructions.  Two register sets in turn need the code twice, which cost more than the
-// latency it hid.)
+// tile before are stored; its rows are in L2 by then.  Bound by instructions: 16 warps that
+// each found their own rows issued 2200 of 9900 instructions a tile for it (600 us on the chunk
+// of 1024 queries x 1152 rows, 580 so).  (8 warps with 8 rows each took twice as long over a
+// tile; a second set of registers, one tile further ahead, measured 584 us.)
 __device__ __forceinline__ void gather(const Args& a, const Shared& sh) {
   uint8_t* smem = sh.smem;
   const int pw = (threadIdx.x >> 5) - kLoad0, lane = threadIdx.x & 31;
@@ -575,7 +584,7 @@ __device__ __forceinline__ void gather(const Args& a, const Shared& sh) {
   }
 }
 
-// ------------------------------------------------------------------ bf16 copy (2 warps)
+// ------------------------------------------------------------------ rows and bf16 copy (2 warps)
 
 // A line of 64 channels after another of Q's row r: in L2 when its turn comes.
 __device__ __forceinline__ void prefetch_q(const Args& a, int item, int r) {
@@ -655,7 +664,9 @@ __device__ __forceinline__ void copy_rows(const Args& a, const Shared& sh) {
 
 // ------------------------------------------------------------------ softmax (4 warps)
 
-// A thread has rows 16 w + lane / 4 and the one 8 below, 16 columns of each.
+// A thread has rows 16 w + lane / 4 and the one 8 below, 16 columns of each.  (8 warps, two to
+// a row that exchange maxima, left the others too few registers and issue slots: 654 against
+// 600 us on the chunk of 1024 queries x 1152 rows.)
 __device__ __forceinline__ void softmax(const Args& a, const Shared& sh) {
   uint8_t* smem = sh.smem;
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -932,7 +943,8 @@ __device__ __forceinline__ void issue_mmas(const Args& a, const Shared& sh) {
   uint32_t first_bits = 0;        // tile & 1: first of its segment
   // Two S, then the two P K: while the softmax of one tile runs the tensor cores have the
   // other, and a tile's place in the ring is refilled during the second P K.  A segment's
-  // first S waits for its Q, so what is pending goes first.
+  // first S waits for its Q, so what is pending goes first.  (Polling for whichever can go
+  // measured 607 against 600 us on the chunk of 1024 queries x 1152 rows.)
   bool ok = true;
   while (ok) {
     while (ok && s < pv + 2) {
@@ -1146,8 +1158,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 // by the parts' bytes (fp32, from L2 as a rule) and by three dependent round trips, so all of
 // it should be resident at once.  (A block for every head of every CTA boundary, most of
 // them idle, took 26 to 40 us.)
-constexpr int kMaxParts = 160;   // CTAs, with room
-constexpr int kFewParts = 16;   // two lanes for each
+constexpr int kMaxParts = 160;  // CTAs, with room
+// Parts up to which a warp takes them one after the other (at most 16, two lanes for each): 64
+// queries split in two 267 us so and 380 with a block a head pair; 5 parts 21.6 and 18.4, 3 to
+// 9 parts 26.7 and 21.3.
+constexpr int kFewParts = 4;
 constexpr int kJoinWarps = 4;
 
 struct Split {
@@ -1329,8 +1344,20 @@ __global__ void __launch_bounds__(128 * kJoinGroups) attention_join_many_kernel(
 
 constexpr int kMaxCtas = 148;        // SMs: one CTA each
 static_assert(kMaxCtas <= kMaxParts, "a query may be split among all CTAs");
-constexpr int kMinTiles = 2;         // tiles per CTA below which a query is not split further
-constexpr int64_t kStridedItems = 8; // items per CTA from which queries are never split
+// Tiles of a part at least, however few the queries (512 + 128 rows, one query: 18.4 us with 2,
+// 29.0 with 1, 22.0 with 3), and more in long queries, whose join takes longer the more parts
+// there are (8320 rows, one query of two groups: 32.0 us with 2, 30.0 with 3).
+constexpr int kMinTiles = 2;
+int least_tiles(int tiles_per_item) {
+  int n = kMinTiles;
+  while (16 * n * n < tiles_per_item) ++n;  // sqrt(tiles) / 4
+  return n;
+}
+// Queries go whole, CTA by CTA, where the CTAs that get one less wait for few tiles.  Splitting
+// evens that out but costs the parts' way through memory and the join, 20 to 25 us: with 128
+// queries of 1152 rows (256 items, idle for 5 tiles on average) 96 us whole and 102 split, with
+// 700 (9.7 tiles) 422 either way, with 300 (17 tiles) 214 whole and 199 split.
+constexpr int64_t kIdleTiles = 8;
 
 struct Plan {
   int64_t items, units;
@@ -1343,12 +1370,13 @@ Plan plan_of(int64_t T, int H, int64_t most, int max_ctas) {
   p.items = T * p.groups;
   p.tiles_per_item = most > 0 ? static_cast<int>(ceil_div(most, kRows)) : 1;
   p.units = p.items * p.tiles_per_item;
-  // (unit numbers are 32-bit)
-  p.strided = p.items >= kStridedItems * max_ctas || p.units > 0x7fffffff - 2 * kMaxCtas;
+  // (decided for the full machine, as the workspace is; unit numbers are 32-bit)
+  const int64_t idle = (ceil_div(p.items, kMaxCtas) * kMaxCtas - p.items) * p.tiles_per_item;
+  p.strided = idle <= kIdleTiles * kMaxCtas || p.units > 0x7fffffff - 2 * kMaxCtas;
   if (p.strided) {
-    p.ctas = max_ctas;
+    p.ctas = static_cast<int>(p.items < max_ctas ? p.items : max_ctas);
   } else {
-    int64_t c = p.units / kMinTiles;
+    int64_t c = p.units / least_tiles(p.tiles_per_item);
     if (c < p.items) c = p.items;
     p.ctas = static_cast<int>(c < max_ctas ? c : max_ctas);
   }

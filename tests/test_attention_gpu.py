@@ -547,7 +547,8 @@ def test_decode_step_together():
 
 
 @pytest.mark.parametrize("T,H,n", [(1, 130, 9000), (1, 7, 20000), (2, 65, 5000), (3, 1, 12000),
-                                   (40, 66, 500), (100, 128, 300), (149, 64, 190)])
+                                   (40, 66, 500), (100, 128, 300), (149, 64, 190), (40, 66, 2000),
+                                   (100, 128, 1500), (149, 64, 900), (1, 64, 640)])
 def test_split_queries_and_the_bounds_of_the_workspace(T, H, n):
     """Queries in two to more than a hundred parts, odd heads, several head groups; a workspace
     of exactly the stated bytes, full of NaN patterns, between guards."""
@@ -555,7 +556,7 @@ def test_split_queries_and_the_bounds_of_the_workspace(T, H, n):
     p = Problem(T, H, 512, 64, [3] * T, lens, seed=T + H, sink=True,
                 window=([0] * T, [t % 9 for t in range(T)], 8))
     need = kvc.shared_kv_attention_workspace_bytes(T, H, 512, 64, n + 8)
-    assert need > 0
+    assert need > 0 or n <= 500  # (0: short queries of a fairly full machine go whole)
     buf = torch.full((need + 8192,), 0xFF, dtype=torch.uint8, device="cuda")
     out, lse = p.run(workspace=buf[4096: 4096 + need])
     assert kvc.device_status() == kvc.KVC_OK
@@ -568,8 +569,8 @@ def test_split_queries_and_the_bounds_of_the_workspace(T, H, n):
 @pytest.mark.parametrize("listed", [False, True])
 @pytest.mark.parametrize("T", [591, 592, 1300])
 def test_many_queries_on_both_sides_of_whole_query_scheduling(T, listed):
-    """Two head groups each: 1182, 1184 and 2600 items, the CTAs' ranges below 1184 and whole
-    items in turn from there; empty queries and windows among them, outputs between guards."""
+    """Two head groups each: 1182, 1184 and 2600 items in turn on 148 CTAs, a full last round or
+    not; empty queries and windows among them, outputs between guards."""
     rng = np.random.default_rng(T)
     lens = [(t * 31) % 140 for t in range(T)]
     idx = _lists(rng, lens, 70, holes=0.1) if listed else None
