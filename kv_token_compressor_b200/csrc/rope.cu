@@ -7,7 +7,10 @@
 // every head it handles; the rotation itself is 3 flops a value, so the kernel is bound by
 // memory traffic (long calls) or by launch and one dependent round trip (short ones).  A unit
 // is one vector of up to 16 bytes (half layout: the vector and its partner r / 2 channels on);
-// every thread has all its kUnits loads in flight before the angles are formed.
+// every thread has all its kUnits loads in flight before the angles are formed.  Measured:
+// 4096 x 128 heads, r = 64 in place (134 MB) 21.6 us, 0.95 of the copy bandwidth; 128 x 128
+// heads 3.2 us and one token 2.4 us, a launch and its round trip; fp32 777 x 24 heads of 192
+// (29 MB, out of place) 6.9 us against 4.4 at the copy bandwidth.
 #include <math.h>
 
 #include "kvc_common.cuh"

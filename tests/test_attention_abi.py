@@ -217,3 +217,8 @@ def test_limits_of_what_the_kernels_hold(L):
     assert att(L, sel=((1 << 31) - 64,), mw=0, q=None) == kvc.KVC_ERR_NULL
     assert att(L, sel=((1 << 31) - 63,), mw=0, q=None) == kvc.KVC_ERR_UNSUPPORTED
     assert att(L, sel=((1 << 31) - 64,), mw=1, q=None) == kvc.KVC_ERR_UNSUPPORTED
+
+
+def test_binding_refuses_a_window_without_starts():
+    with pytest.raises(ValueError, match="win_start"):
+        kvc.shared_kv_attention(**_args(window=_win(2, None)))
