@@ -453,8 +453,8 @@ struct RowCursor {
 // has rows [4 pw, 4 pw + 4) of a tile, a lane the 8-channel chunks lane and lane + 32 of each
 // (a warp reads 256 consecutive bytes).  A tile's loads set out as soon as the registers of the
 // tile before are stored; its rows are in L2 by then.  Bound by instructions: 16 warps that
-// each found their own rows issued 2200 of 9900 instructions a tile for it (600 us on the chunk
-// of 1024 queries x 1152 rows, 580 so).  (8 warps with 8 rows each took twice as long over a
+// each found their own rows issued a third of 9900 instructions a tile for it (6450 now; 600 us
+// on the chunk of 1024 queries x 1152 rows, 580 so).  (8 warps with 8 rows each took twice as long over a
 // tile; a second set of registers, one tile further ahead, measured 584 us.)
 __device__ __forceinline__ void gather(const Args& a, const Shared& sh) {
   uint8_t* smem = sh.smem;

@@ -8,9 +8,10 @@
 // memory traffic (long calls) or by launch and one dependent round trip (short ones).  A unit
 // is one vector of up to 16 bytes (half layout: the vector and its partner r / 2 channels on);
 // every thread has all its kUnits loads in flight before the angles are formed.  Measured:
-// 4096 x 128 heads, r = 64 in place (134 MB) 21.6 us, 0.95 of the copy bandwidth; 128 x 128
-// heads 3.2 us and one token 2.4 us, a launch and its round trip; fp32 777 x 24 heads of 192
-// (29 MB, out of place) 6.9 us against 4.4 at the copy bandwidth.
+// 4096 x 128 heads, r = 64 of c = 512 in place (134 MB, 128 of every 1024 bytes) 29.0 us, 0.71 of
+// the copy bandwidth (1, 2 and 8 units a thread: 36.8, 29.0, 31.4; streaming loads and stores
+// 28.8); 128 x 128 heads 3.2 us and one token 2.4 us, a launch and its round trip; fp32 777 x 24
+// heads of 192 (29 MB, out of place) 6.9 us against 4.4 at the copy bandwidth.
 #include <math.h>
 
 #include "kvc_common.cuh"
