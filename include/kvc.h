@@ -482,8 +482,8 @@ KVC_API const char* kvc_last_kernel(void);
  * KVC_ERR_TIMEOUT if a bounded wait gave up (this takes precedence); else
  * KVC_ERR_WORKSPACE if a prepared-bias workspace did not match its call; else KVC_ERR_INDEX if
  * an entry list, an indexer window or an attention call's ranges or lists named rows outside
- * its sequence or the arrays; else KVC_OK.  The words belong to the current device, not to a stream or a host thread: they
- * collect what every kernel of this library set since the last call, and one call clears
+ * its sequence or the arrays; else KVC_OK.  The words belong to the current device, not to a
+ * stream or a host thread: they collect what every kernel of this library set since the last call, and one call clears
  * them for all callers. */
 KVC_API kvc_status kvc_device_status(kvc_stream stream);
 

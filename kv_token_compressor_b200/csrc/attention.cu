@@ -22,11 +22,12 @@
 // exchange cross the SM-to-SM network at 20 bytes a cycle and its latency (about 4000 cycles)
 // sits in every tile's chain: 5300 cycles a tile.
 //
-// What a tile takes: 4300 cycles (chunk of 1024 queries x 1152 rows x 128 heads: 580 us, 525
+// What a tile takes: 4250 cycles (chunk of 1024 queries x 1152 rows x 128 heads: 574 us, 530
 // TFLOP/s).  With every load, conversion, exponential and store taken out 3100 remain, and the
 // hand-overs alone (no MMAs either) take 1000: S of a tile, its softmax, P K and the refill of
 // its place follow one another, two tiles in turn, and S reads Q and K from shared memory at
-// nearly all the bytes a cycle that it has, so that everything beside it waits.
+// nearly all the bytes a cycle that it has, so that everything beside it waits: a wait that is
+// over already takes 170 to 250 cycles.  So no barrier stands where another one implies it.
 //
 // Types.  An E4M3 byte is exact in fp16, and a bf16 query row is exact in fp16 once scaled by
 // a power of two (its largest value to 2^15: what is lost lies 2^-40 below it), so the FP8
@@ -114,14 +115,14 @@ constexpr int kSmMisc = kSmMask + kStages * 8;       // tmem address, abort flag
 constexpr int kSmBars = kSmMisc + 8;
 // mbarriers, by index
 constexpr int kBKFull = 0;                  // [kStages] a row tile is in place
-constexpr int kBKEmpty = kBKFull + kStages; // [kStages] the MMAs are done with it
+constexpr int kBKEmpty = kBKFull + kStages; // [kStages] the MMAs are done with it:
+constexpr int kBPvDone = kBKEmpty;          // O includes the tile, its weights have been used
+static_assert(kStages == 2, "as many as S and weight buffers");
 constexpr int kBQFull = kBKEmpty + kStages; // Q in place (per segment)
 constexpr int kBQEmpty = kBQFull + 1;       // the MMAs are done with Q
 constexpr int kBSFull = kBQEmpty + 1;       // [2] S complete
-constexpr int kBSFree = kBSFull + 2;        // [2] S has been read
-constexpr int kBPFull = kBSFree + 2;        // [2] weights in place
-constexpr int kBPvDone = kBPFull + 2;       // [2] O includes the tile
-constexpr int kBOFree = kBPvDone + 2;       // O has been read (per segment)
+constexpr int kBPFull = kBSFull + 2;        // [2] weights in place, S has been read
+constexpr int kBOFree = kBPFull + 2;        // O has been read (per segment)
 constexpr int kBLFull = kBOFree + 1;        // [kSegs] (m, l) posted
 constexpr int kBSegFull = kBLFull + kSegs;  // [kSegs] a segment record is posted
 constexpr int kBSegEmpty = kBSegFull + kSegs;  // [kSegs] every role has read it
@@ -689,10 +690,21 @@ __device__ __forceinline__ void softmax(const Args& a, const Shared& sh) {
 #pragma unroll 1
     for (int i = 0; i < nt; ++i, ++g) {
       const uint32_t b = g & 1u, n = g >> 1, st = g % kStages;
-      if (!sh.wait(kBSFull + b, n & 1u) ||
-          !sh.wait(kBKFull + st, (g / kStages) & 1u))  // (complete: for the mask)
-        return;
+      if (!sh.wait(kBSFull + b, n & 1u)) return;
       tc_fence_after();
+      float x[32], u[32];
+      const uint32_t sb = lane_addr + kColS + 64 * b;
+      float2 (&x2)[16] = *reinterpret_cast<float2(*)[16]>(x);  // [2 k + row]: two columns
+      const float2(&u2)[16] = *reinterpret_cast<const float2(*)[16]>(u);
+      if (na > 0) {
+        tmem_ld_rows(sb, x);
+        if (nr > 0) tmem_ld_rows(sb + kUpper, u);
+      } else {
+        tmem_ld_rows(sb + kUpper, x);
+      }
+      // (complete since S is: for the mask's sight, while the loads are under way)
+      const bool there = sh.wait(kBKFull + st, (g / kStages) & 1u);
+      const uint2 live = *reinterpret_cast<const uint2*>(smem + kSmMask + st * 8);
       if (i == 0) {
         // x = S_n * (2^(E - 142) scale / fp8_scale) + S_r * scale, in units of log 2
 #pragma unroll
@@ -701,34 +713,19 @@ __device__ __forceinline__ void softmax(const Args& a, const Shared& sh) {
           scale_n[r] = n_scale * __int_as_float((e - 15) << 23);
         }
       }
-      const uint2 live = *reinterpret_cast<const uint2*>(smem + kSmMask + st * 8);
-      float x[32];
-      const uint32_t sb = lane_addr + kColS + 64 * b;
-      float2 (&x2)[16] = *reinterpret_cast<float2(*)[16]>(x);  // [2 k + row]: two columns
-      if (na > 0) {
-        tmem_ld_rows(sb, x);
-        float u[32];
-        const float2(&u2)[16] = *reinterpret_cast<const float2(*)[16]>(u);
-        if (nr > 0) tmem_ld_rows(sb + kUpper, u);
-        tmem_wait_ld();
-        if (nr > 0) {
+      tmem_wait_ld();
+      if (!there) return;
+      if (na > 0 && nr > 0) {
 #pragma unroll
-          for (int c = 0; c < 16; ++c)
-            x2[c] = f2_fma(x2[c], make_float2(scale_n[c & 1], scale_n[c & 1]),
-                           f2_mul(u2[c], make_float2(b_scale, b_scale)));
-        } else {
-#pragma unroll
-          for (int c = 0; c < 16; ++c)
-            x2[c] = f2_mul(x2[c], make_float2(scale_n[c & 1], scale_n[c & 1]));
-        }
+        for (int c = 0; c < 16; ++c)
+          x2[c] = f2_fma(x2[c], make_float2(scale_n[c & 1], scale_n[c & 1]),
+                         f2_mul(u2[c], make_float2(b_scale, b_scale)));
       } else {
-        tmem_ld_rows(sb + kUpper, x);
-        tmem_wait_ld();
+        const float f0 = na > 0 ? scale_n[0] : b_scale, f1 = na > 0 ? scale_n[1] : b_scale;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) x2[c] = f2_mul(x2[c], make_float2(b_scale, b_scale));
+        for (int c = 0; c < 16; ++c)
+          x2[c] = f2_mul(x2[c], c & 1 ? make_float2(f1, f1) : make_float2(f0, f0));
       }
-      tc_fence_before();
-      sh.arrive(kBSFree + b);
       if ((live.x & live.y) != ~0u) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -772,8 +769,8 @@ __device__ __forceinline__ void softmax(const Args& a, const Shared& sh) {
         tmem_wait_st();
         tc_fence_before();
       }
-      // the weights of the tile two before this one have been used
-      if (g >= 2 && !sh.wait(kBPvDone + b, (n - 1) & 1u)) return;
+      // (the weights of the tile two before this one have been used: its P K was issued before
+      // S of this one, whose commit covers both)
       uint8_t* pb = prow + b * 2 * kAtom;
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -791,6 +788,7 @@ __device__ __forceinline__ void softmax(const Args& a, const Shared& sh) {
       }
 #pragma unroll
       for (int r = 0; r < 2; ++r) l[r] += sum[r].x + sum[r].y;
+      tc_fence_before();
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       sh.arrive(kBPFull + b);
     }
@@ -964,10 +962,9 @@ __device__ __forceinline__ void issue_mmas(const Args& a, const Shared& sh) {
       if (!ok || ended || (first && pv < s)) break;
       const uint32_t b = s & 1u, st = s % kStages;
       ok = (!first || wait(kBQFull, s_seg & 1u)) &&
-           (s < 2 || wait(kBSFree + b, ((s >> 1) - 1) & 1u)) &&
            wait(kBKFull + st, (s / kStages) & 1u);
       if (!ok) break;
-      tc_fence_after();
+      tc_fence_after();  // (S of the tile two before has been read: its weights were there)
       const uint32_t dt = tmem + kColS + 64 * b;
 #pragma unroll 1
       for (int at = 0; at < blocks; ++at) {
@@ -1010,7 +1007,6 @@ __device__ __forceinline__ void issue_mmas(const Args& a, const Shared& sh) {
                     idesc(true, true, nr_hi * 64), acc);
       }
       umma_commit(bars + kBKEmpty + st);
-      umma_commit(bars + kBPvDone + b);
       if (begins) ++pv_seg;
       ++pv;
     }
@@ -1096,7 +1092,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       uint32_t count = 1;  // commits, the scheduler
       if (i >= kBKFull && i < kBKFull + kStages) count = kLoadWarps + 2;
       if (i == kBQFull) count = kLoadWarps;
-      if (i >= kBSFree && i < kBSFree + 2) count = kSoftWarps;
       if (i >= kBPFull && i < kBPFull + 2) count = kSoftWarps;
       if (i == kBOFree) count = kStoreWarps;
       if (i >= kBLFull && i < kBLFull + kSegs) count = kSoftWarps;
