@@ -87,14 +87,14 @@ constexpr int kAtom = 64 * 128;   // one [64 rows or heads x 64] block of 16-bit
 constexpr int kStage = kMaxAtoms * kAtom;
 constexpr int kSegs = 8;          // segment records under way
 constexpr int kExps = 4;          // and exponents of Q rows
-// Bounded waits: polls before a wait gives up (each tens of cycles at least, so a few tenths of
-// a second; a sound run waits microseconds, except for the end of a segment, which may wait
-// kTilePolls more for each of its tiles).  Reading the nanosecond timer between polls took
-// thousands of cycles and made every wait that long.
-constexpr uint32_t kSpinLimit = 1u << 18;
-constexpr uint32_t kTilePolls = 1u << 9;
-constexpr int kTilesCounted = 1 << 22;  // (2^31 polls at most)
-constexpr long long kSchedLimit = 200000000000ll;  // cycles: a record may wait for long segments
+// Bounded waits: every wait of a CTA gives up once the CTA has not gone on for kWaitTicks ticks
+// of 2^16 cycles (2 to 3 s).  It goes on when the softmax of a tile ends (microseconds) and when
+// the scheduler or a store warp walks over a query, so neither a long query (many tiles before
+// the store warps' next output) nor a padded batch (2^28 queries of which six have rows: 4.2 s
+// in which the other roles have nothing to do; a limit of 2^18 polls gave up there) is taken for
+// a standstill.  The cycle counter is read at every 16th poll of a wait; reading the nanosecond
+// timer between polls took thousands of cycles and made every wait that long.
+constexpr uint32_t kWaitTicks = 1u << 16;
 // Weights are exp2(x - m + kBias): with m at most kSlack below the running maximum they stay
 // below 2^15 in fp16 and vanish only 2^-31 below the maximum.
 constexpr float kBias = 7.f;
@@ -110,8 +110,8 @@ constexpr int kSmRow = kSmSeg + kSegs * int(sizeof(Seg));  // u64 [2][kRows] whe
 constexpr int kSmMl = kSmRow + 2 * kRows * 8;        // float2 [kHeads] (m, l)
 constexpr int kSmExp = kSmMl + kHeads * 8;           // u8 [kExps][kHeads] exponents of Q rows
 constexpr int kSmMask = kSmExp + kExps * kHeads;     // u32 [kStages][2] rows that count
-constexpr int kSmMisc = kSmMask + kStages * 8;       // tmem address, abort flag
-constexpr int kSmBars = kSmMisc + 8;
+constexpr int kSmMisc = kSmMask + kStages * 8;       // tmem address, abort flag, tick of the last step
+constexpr int kSmBars = kSmMisc + 16;
 // mbarriers, by index
 constexpr int kBKFull = 0;                  // [kStages] a row tile is in place
 constexpr int kBKEmpty = kBKFull + kStages; // [kStages] the MMAs are done with it:
@@ -328,33 +328,33 @@ __device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+__device__ __forceinline__ uint32_t ticks() { return static_cast<uint32_t>(clock64() >> 16); }
+// Whether the CTA has stood still for too long, or has been told to stop.  abort_flag[1]: the
+// tick at which it last went on.
+__device__ __forceinline__ bool gave_up(volatile int* abort_flag) {
+  const uint32_t last = static_cast<uint32_t>(abort_flag[1]);
+  // (signed: another warp may note a later tick than this thread's between the two reads)
+  if (static_cast<int32_t>(ticks() - last) > static_cast<int32_t>(kWaitTicks)) {
+    *abort_flag = 1;
+    atomicOr(&g_attention_error, 1u);
+  }
+  return *abort_flag != 0;
+}
 // Bounded wait of a whole warp; one answer for its lanes.  (No function call: calls do not go
 // with setmaxnreg.)
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                          uint32_t limit = kSpinLimit) {
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity,
+                                          volatile int* abort_flag) {
 #pragma unroll 1
-  for (uint32_t spins = 1;; ++spins) {
-    if (__all_sync(0xffffffffu, try_wait_long(bar, parity))) return true;
-    if (spins % 16 != 0) continue;
-    if (spins >= limit) {
-      *abort_flag = 1;
-      atomicOr(&g_attention_error, 1u);
-    }
-    if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
-  }
+  for (uint32_t spins = 1; !__all_sync(0xffffffffu, try_wait_long(bar, parity)); ++spins)
+    if (spins % 16 == 0 && __any_sync(0xffffffffu, gave_up(abort_flag))) return false;
+  return true;
 }
 // The same for one thread.
 __device__ __forceinline__ bool wait_thread(uint64_t* bar, uint32_t parity,
                                             volatile int* abort_flag) {
 #pragma unroll 1
-  for (uint32_t spins = 1; !try_wait_long(bar, parity); ++spins) {
-    if (spins % 16 != 0) continue;
-    if (spins >= kSpinLimit) {
-      *abort_flag = 1;
-      atomicOr(&g_attention_error, 1u);
-    }
-    if (*abort_flag) return false;
-  }
+  for (uint32_t spins = 1; !try_wait_long(bar, parity); ++spins)
+    if (spins % 16 == 0 && gave_up(abort_flag)) return false;
   return true;
 }
 // One lane of a converged warp, in the form the compiler knows to leave a single thread: the
@@ -388,6 +388,8 @@ struct Shared {
   __device__ __forceinline__ bool wait(int bar, uint32_t parity) const {
     return wait_warp(bars + bar, parity, abort_flag);
   }
+  // the CTA goes on (see the bounded waits)
+  __device__ __forceinline__ void went_on() const { abort_flag[1] = static_cast<int>(ticks()); }
   // one arrival for a warp, after all its lanes got here
   __device__ __forceinline__ void arrive(int bar) const {
     __syncwarp();
@@ -792,6 +794,7 @@ __device__ __forceinline__ void softmax(const Args& a, const Shared& sh) {
       tc_fence_before();
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       sh.arrive(kBPFull + b);
+      if (threadIdx.x == 0) sh.went_on();
     }
     // the sums of the segment before this one have been read
     if (seg > 0 && !sh.wait(kBOFree, (seg - 1) & 1u)) return;
@@ -826,13 +829,13 @@ __device__ __forceinline__ void store_out_rows(const Args& a, const Shared& sh) 
     const int nt = q.j1 - q.j0, hg = q.hg, part = q.part;
     const bool ok = q.ok;
     if (t < 0) return;
+    if (lane == 0) sh.went_on();
     if (!ok && w == 0 && lane == 0) atomicOr(&g_attention_error, 2u);
     float m = -INFINITY, l = 0.f;
     if (nt > 0) {
       g += nt;
       const uint32_t gl = g - 1;
-      if (!wait_warp(sh.bars + kBLFull + seg % kSegs, (seg / kSegs) & 1u, sh.abort_flag,
-                     kSpinLimit + kTilePolls * min(nt, kTilesCounted)) ||
+      if (!sh.wait(kBLFull + seg % kSegs, (seg / kSegs) & 1u) ||
           !sh.wait(kBPvDone + (gl & 1u), (gl >> 1) & 1u))
         return;
       tc_fence_after();
@@ -1013,7 +1016,7 @@ __device__ __forceinline__ void issue_mmas(const Args& a, const Shared& sh) {
     }
   }
   umma_commit(bars + kBFinal);  // every MMA issued above has finished before TMEM is freed
-  for (uint32_t i = 0; i < kSpinLimit && !try_wait_long(bars + kBFinal, 0); ++i) {
+  for (const uint32_t t0 = ticks(); !try_wait_long(bars + kBFinal, 0) && ticks() - t0 < kWaitTicks;) {
   }
 }
 
@@ -1027,15 +1030,10 @@ __device__ __forceinline__ void schedule(const Args& a, const Shared& sh) {
     Seg q;
     do {
       q = next_segment(a, &at, end);
+      sh.went_on();
     } while (q.t >= 0 && q.j0 == q.j1);
-    const long long t0 = clock64();
-    while (!mbar_try_wait(sh.bars + kBSegEmpty + sn % kSegs, ((sn / kSegs) & 1u) ^ 1u)) {
-      if (clock64() - t0 > kSchedLimit) {
-        *sh.abort_flag = 1;
-        atomicOr(&g_attention_error, 1u);
-      }
-      if (*sh.abort_flag) return;
-    }
+    if (!wait_thread(sh.bars + kBSegEmpty + sn % kSegs, ((sn / kSegs) & 1u) ^ 1u, sh.abort_flag))
+      return;
     segs[sn % kSegs] = q;
     mbar_arrive(sh.bars + kBSegFull + sn % kSegs);
     if (q.t < 0) return;
@@ -1102,6 +1100,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       mbar_init(sh.bars + i, count);
     }
     *sh.abort_flag = 0;
+    sh.went_on();
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
