@@ -391,8 +391,9 @@ typedef enum kvc_rope_layout {
  *   r > 32768 or more than 2^30 16-byte units a token: KVC_ERR_UNSUPPORTED
  *   out == x works in place (only the last r channels are then touched); any other overlap
  *   of x and out returns KVC_ERR_POINTER.
- * The angle is formed and reduced modulo 2 pi in fp64, its sine and cosine and the rotation
- * in fp32; bf16 results are rounded once. */
+ * The angle is formed and reduced modulo 2 pi in fp64; its sine and cosine are fp32, within
+ * 2.5 units in the last place of that angle's own; the rotation is fp32; bf16 results are
+ * rounded once. */
 KVC_API kvc_status partial_rope(const void* x, void* out, kvc_dtype dtype, int64_t T, int32_t H,
                                 int64_t c, int32_t r, const int64_t* pos, const float* inv_freq,
                                 int32_t layout, int32_t inverse, float magnitude,

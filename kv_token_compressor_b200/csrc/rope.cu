@@ -106,9 +106,14 @@ __global__ void __launch_bounds__(kThreads) partial_rope_kernel(const Args a) {
     const double turns = rint(ang * 0.15915494309189535);
     const double red =
         fma(-turns, 2.4492935982947064e-16, fma(-turns, 6.283185307179586, ang));
+    // what the angle loses in fp32 (up to 2^-23, all of a sine next to a multiple of pi) is put
+    // back by the first term of the addition theorem: sin(h + l) = sin h + l cos h to 2^-47
+    const float high = static_cast<float>(red);
+    const float low = static_cast<float>(red - high);
     float sn, cn_;
-    sincosf(static_cast<float>(red), &sn, &cn_);
-    cs[p] = make_float2(cn_ * a.magnitude, sn * a.magnitude * a.sign);
+    sincosf(high, &sn, &cn_);
+    const float s_ = fmaf(low, cn_, sn), c_ = fmaf(-low, sn, cn_);
+    cs[p] = make_float2(c_ * a.magnitude, s_ * a.magnitude * a.sign);
   }
   __syncthreads();
 #pragma unroll
