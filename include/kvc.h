@@ -452,7 +452,7 @@ KVC_API kvc_status kvc_rope_frequencies(int32_t r, double base, double factor, d
  *   max_win; it holds the partial sums of queries whose rows are split among the GPU's
  *   processors.  Nothing in it outlives the call; calls whose work may overlap on the GPU
  *   need one each (two captured graphs that may run at once included).  0 bytes: it is not
- *   used and may be NULL.
+ *   used and may be NULL; -1: the call refuses these sizes.
  *   The result does not depend on what else runs: each sum has a fixed order. */
 KVC_API int64_t shared_kv_attention_workspace_bytes(int64_t T, int32_t H, int64_t c, int32_t r,
                                                     int64_t most_rows);

@@ -1397,7 +1397,6 @@ kvc_status launch_attention(const AttentionProblem& p, cudaStream_t st) {
   if (sms < 1) return KVC_ERR_CUDA;
   const int64_t most = (p.idx ? p.k : p.max_visible) + (p.win_start ? p.max_win : 0);
   const Plan pl = plan_of(p.T, p.H, most, sms < kMaxCtas ? sms : kMaxCtas);
-  if (pl.items > 0x7fffffff - 2 * kMaxCtas) return KVC_ERR_UNSUPPORTED;
   Args a{};
   a.p = p;
   a.items = static_cast<int>(pl.items);

@@ -147,6 +147,13 @@ kvc_status attention_shape(int64_t T, int32_t H, int64_t c, int32_t r) {
   return KVC_OK;
 }
 
+// Whether the rows of a query and the (query, 64 heads) pairs of a checked shape fit the kernels'
+// 32-bit counts.
+bool attention_counts_fit(int64_t T, int32_t H, int64_t most) {
+  return most <= (int64_t(1) << 31) - 64 &&
+         T * kvc::ceil_div(H, 64) < (int64_t(1) << 31) - 300;
+}
+
 // Checks and launches a shared-KV attention problem (idx counts only with `listed`).
 kvc_status attention_call(const kvc::AttentionProblem& p, bool listed, int64_t workspace_bytes,
                           cudaStream_t st) {
@@ -170,7 +177,7 @@ kvc_status attention_call(const kvc::AttentionProblem& p, bool listed, int64_t w
   int64_t most = listed ? p.k : p.max_visible;
   if (win && __builtin_add_overflow(most, p.max_win, &most)) return KVC_ERR_SHAPE;
   if (p.T == 0) return KVC_OK;
-  if (most > (int64_t(1) << 31) - 64) return KVC_ERR_UNSUPPORTED;  // 32-bit row counts
+  if (!attention_counts_fit(p.T, p.H, most)) return KVC_ERR_UNSUPPORTED;
   const bool rows = p.cache_rows > 0, wrows = win && p.win_rows > 0;
   if (!p.q || !p.out || !p.key_start || !p.n_visible || (listed && !p.idx)) return KVC_ERR_NULL;
   if ((rows && ((cn > 0 && !p.nope) || (r > 0 && !p.rope))) || (win && !p.win_len) ||
@@ -1062,6 +1069,7 @@ int64_t shared_kv_attention_workspace_bytes(int64_t T, int32_t H, int64_t c, int
                                             int64_t most_rows) {
   if (T < 0 || most_rows < 0 || attention_shape(T, H, c, r) != KVC_OK) return -1;
   if (T == 0) return 0;
+  if (!attention_counts_fit(T, H, most_rows)) return -1;
   return kvc::attention_workspace_bytes(T, H, c, r, most_rows);
 }
 
