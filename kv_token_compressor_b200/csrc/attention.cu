@@ -276,9 +276,6 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint2 lo, uint2 hi) {
                "r"(hi.x), "r"(hi.y)
                : "memory");
 }
-__device__ __forceinline__ void st_shared4(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
 __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
