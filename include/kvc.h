@@ -445,8 +445,18 @@ KVC_API kvc_status kvc_rope_frequencies(int32_t r, double base, double factor, d
  *   whose win_len leaves [0, max_win], or one of whose groups leaves its arrays, is skipped
  *   (out and lse rows untouched); a listed entry outside [-1, n_visible[t]) is left out of
  *   the sums.  kvc_device_status() then reports KVC_ERR_INDEX.
- * Arithmetic: E4M3 and bf16 operands are widened exactly; dot products, softmax statistics
- *   and output sums are fp32; bf16 outputs are rounded once.
+ * Arithmetic: dot products, softmax statistics (m, D) and output sums are fp32; bf16 outputs
+ *   are rounded once.  Cache values are exact.  Two operands are held in 16 bits:
+ *   - each weight exp(x_s) is rounded to fp16 (by at most 2^-11 of itself, or 2^-32 of the
+ *     largest if that is more) where it
+ *     multiplies FP8 channels and to bf16 (2^-8) where it multiplies bf16 channels, so with
+ *     r == c every output carries the 8-bit rounding.  The roundings of a query's rows are
+ *     independent and average out: the error's root mean square is about 0.43 x 2^-11 (FP8
+ *     channels) or 0.43 x 2^-8 (bf16 channels) of sqrt(sum_s p_s^2 K_s^2), p_s = exp(x_s) / D.
+ *     D and lse are sums of the unrounded weights;
+ *   - against FP8 channels a query's q is fp16 times a power of two that puts its largest
+ *     FP8 channel at 2^15 to 2^16: exact down to 2^-32 of that channel, off by at most 2^-40
+ *     of it below.
  * workspace: device memory, 256-byte aligned, at least
  *   shared_kv_attention_workspace_bytes(T, H, c, r, most) with most = max_visible (or k) +
  *   max_win; it holds the partial sums of queries whose rows are split among the GPU's
