@@ -447,10 +447,10 @@ KVC_API kvc_status kvc_rope_frequencies(int32_t r, double base, double factor, d
  *   the sums.  kvc_device_status() then reports KVC_ERR_INDEX.
  * Arithmetic: dot products, softmax statistics (m, D) and output sums are fp32; bf16 outputs
  *   are rounded once.  Cache values are exact.  Two operands are held in 16 bits:
- *   - each weight exp(x_s) is rounded to fp16 (by at most 2^-11 of itself, or 2^-32 of the
- *     largest if that is more) where it
- *     multiplies FP8 channels and to bf16 (2^-8) where it multiplies bf16 channels, so with
- *     r == c every output carries the 8-bit rounding.  The roundings of a query's rows are
+ *   - each weight exp(x_s) is rounded to fp16 where it multiplies FP8 channels (by at most
+ *     2^-11 of itself, or 2^-32 of the largest if that is more) and to bf16 where it
+ *     multiplies bf16 channels (2^-8 of itself), so with r == c every output carries the 8-bit
+ *     rounding.  The roundings of a query's rows are
  *     independent and average out: the error's root mean square is about 0.43 x 2^-11 (FP8
  *     channels) or 0.43 x 2^-8 (bf16 channels) of sqrt(sum_s p_s^2 K_s^2), p_s = exp(x_s) / D.
  *     D and lse are sums of the unrounded weights;
