@@ -653,6 +653,17 @@ def indexer_topk(scores, n_visible, k: int, max_visible: int, out_idx=None, out_
     return out_idx, (out_score if want_scores else None)
 
 
+def _made_on(stream, like, make):
+    """make()'s tensor, from the pool of the stream that the kernels are launched on: a block of
+    the current stream's pool may still be written by work queued there, which the launching
+    stream does not wait for."""
+    if stream is None or not like.is_cuda:
+        return make()
+    torch = _torch()
+    with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=like.device)):
+        return make()
+
+
 _ROPE_LAYOUTS = {"interleaved": KVC_ROPE_INTERLEAVED, "half": KVC_ROPE_HALF}
 
 
@@ -673,7 +684,8 @@ def partial_rope(x, pos, inv_freq, r: int, layout: str = "interleaved", inverse:
                  magnitude: float = 1.0, out=None, stream=None):
     """Rotate the last r channels of x [T, H, c] (bf16 or fp32) by pos[t] * inv_freq[j] (pos
     int64 [T], inv_freq fp32 [r / 2]); inverse=True rotates back (also the gradient of the
-    forward call).  out=x works in place.  Returns out."""
+    forward call).  out=x works in place.  Returns out (made on `stream` if that is given, as
+    under torch.cuda.stream)."""
     torch = _torch()
     code = _ROPE_LAYOUTS.get(layout)
     if code is None:
@@ -681,7 +693,7 @@ def partial_rope(x, pos, inv_freq, r: int, layout: str = "interleaved", inverse:
     T, H, c = x.shape
     dtype = _dtype_code(x.dtype)
     if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        out = _made_on(stream, x, lambda: torch.empty_like(x, memory_format=torch.contiguous_format))
     elif out is not x:
         _out(out, (T, H, c), x.dtype, x)
     ppos = pfreq = None
@@ -747,13 +759,13 @@ def _attention(name, q, nope, rope, key_start, n_visible, idx, most, r, scale, f
     if sink is not None:
         _need("sink", sink, H, torch.float32)
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _made_on(stream, q, lambda: torch.empty_like(q, memory_format=torch.contiguous_format))
     else:
         _out(out, (T, H, c), torch.bfloat16, q)
     if lse is not None:
         _out(lse, (T, H), torch.float32, q)
     elif want_lse:
-        lse = q.new_empty((T, H), dtype=torch.float32)
+        lse = _made_on(stream, q, lambda: q.new_empty((T, H), dtype=torch.float32))
     for t in (key_start, n_visible, ws, wl):
         if t is not None and (t.dtype is not torch.int64 or t.dim() != 1 or t.numel() != T):
             raise ValueError("index arrays must be int64 [num]")
@@ -764,11 +776,7 @@ def _attention(name, q, nope, rope, key_start, n_visible, idx, most, r, scale, f
         given = workspace.numel() * workspace.element_size()
     elif nbytes > 0:
         given = nbytes
-        if stream is None:
-            workspace = q.new_empty((nbytes,), dtype=torch.uint8)
-        else:  # from the launching stream's pool: its reuse is ordered after the kernels
-            with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=q.device)):
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        workspace = _made_on(stream, q, lambda: q.new_empty((nbytes,), dtype=torch.uint8))
     pq, pn, pr, pks, pnv, pwn, pwr, pws, pwl, pidx, psink, pout, plse = ptrs
     selected = (most,) if idx is None else (pidx, most)
     st = getattr(L, name)(pq, T, H, c, r, pn, pr, rows, fp8_scale, pks, pnv, *selected, pwn, pwr,
@@ -786,7 +794,7 @@ def shared_kv_attention(q, nope, rope, key_start, n_visible, max_visible: int, r
     key_start[t] .. + n_visible[t] - 1 of nope [rows, c - r] E4M3 / rope [rows, r] bf16, key and
     value at once), with optional window rows (window = (win_nope, win_rope, win_start,
     win_len, max_win)) and per-head sink logits (fp32 [H]).  Returns (out [T, H, c] bf16,
-    lse fp32 [T, H] or None)."""
+    lse fp32 [T, H] or None), made on `stream` if that is given, as under torch.cuda.stream."""
     return _attention("shared_kv_attention", q, nope, rope, key_start, n_visible, None,
                       int(max_visible), r, scale, fp8_scale, window, sink, out, want_lse, lse,
                       workspace, stream)
