@@ -194,10 +194,24 @@ def _stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _out(out, shape, dtype, like):
+def _made_on(stream, like, make):
+    """make()'s tensor, from the pool of the stream that the kernels are launched on: a block of
+    the current stream's pool may still be written by work queued there, which the launching
+    stream does not wait for."""
+    if stream is None or not like.is_cuda:
+        return make()
+    torch = _torch()
+    with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=like.device)):
+        return make()
+
+
+def _out(out, shape, dtype, like, stream=None):
     torch = _torch()
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        def make():
+            return torch.empty(shape, dtype=dtype, device=like.device)
+
+        return make() if stream is None else _made_on(stream, like, make)
     if out.shape != shape or out.dtype != dtype:
         raise ValueError(f"out must be {tuple(shape)} {dtype}")
     return out
@@ -244,7 +258,7 @@ def csa_compress(Ca, Cb, Za, Zb, Ba, Bb, m: int = 4, overlap: bool = True, out=N
     _streams(Ca, (("Cb", Cb), ("Za", Za), ("Zb", Zb)), ("Cb", "Zb"), overlap)
     _biases(m, c, overlap, Ba=Ba, Bb=Bb)
     out_dtype = Ca.dtype if out_dtype is None else out_dtype
-    out = _out(out, (batch, n // m, c), out_dtype, Ca)
+    out = _out(out, (batch, n // m, c), out_dtype, Ca, stream)
     st = lib().csa_compress(_ptr(Ca), _ptr(Cb) if overlap else None, _ptr(Za),
                             _ptr(Zb) if overlap else None, _dtype_code(Ca.dtype), _ptr(Ba),
                             _ptr(Bb) if overlap else None, batch, n, c, m, int(bool(overlap)),
@@ -259,7 +273,7 @@ def hca_compress(C, Z, B, m: int = 128, out=None, out_dtype=None, stream=None):
     _streams(C, (("Z", Z),), (), True)
     _biases(m, c, True, B=B)
     out_dtype = C.dtype if out_dtype is None else out_dtype
-    out = _out(out, (batch, n // m, c), out_dtype, C)
+    out = _out(out, (batch, n // m, c), out_dtype, C, stream)
     st = lib().hca_compress(_ptr(C), _ptr(Z), _dtype_code(C.dtype), _ptr(B), batch, n, c, m,
                             _ptr(out), _dtype_code(out_dtype), _stream(stream))
     _check(st, "hca_compress")
@@ -279,7 +293,7 @@ def hca_prepare_bias(B, in_dtype, workspace=None, stream=None):
     _need("B", B, m * c, torch.float32)
     nbytes = hca_bias_workspace_bytes(c, m, in_dtype)
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 0), dtype=torch.uint8, device=B.device)
+        workspace = _out(None, (max(nbytes, 0),), torch.uint8, B, stream)
     st = lib().hca_prepare_bias(_ptr(B), c, m, _dtype_code(in_dtype), _ptr(workspace),
                                 workspace.numel() * workspace.element_size(), _stream(stream))
     _check(st, "hca_prepare_bias")
@@ -291,7 +305,7 @@ def hca_compress_prepared(C, Z, workspace, m: int = 128, out=None, out_dtype=Non
     batch, n, c = C.shape
     _streams(C, (("Z", Z),), (), True)
     out_dtype = C.dtype if out_dtype is None else out_dtype
-    out = _out(out, (batch, n // m, c), out_dtype, C)
+    out = _out(out, (batch, n // m, c), out_dtype, C, stream)
     st = lib().hca_compress_prepared(_ptr(C), _ptr(Z), _dtype_code(C.dtype), _ptr(workspace),
                                      workspace.numel() * workspace.element_size(), batch, n, c, m,
                                      _ptr(out), _dtype_code(out_dtype), _stream(stream))
@@ -308,7 +322,7 @@ def hca_compress_noalloc(C, Z, B, m: int = 128, out=None, out_dtype=None, stream
     _streams(C, (("Z", Z),), (), True)
     _biases(m, c, True, B=B)
     out_dtype = C.dtype if out_dtype is None else out_dtype
-    out = _out(out, (batch, n // m, c), out_dtype, C)
+    out = _out(out, (batch, n // m, c), out_dtype, C, stream)
     st = lib().hca_compress_noalloc(_ptr(C), _ptr(Z), _dtype_code(C.dtype), _ptr(B), batch, n, c, m,
                                     _ptr(out), _dtype_code(out_dtype), _stream(stream))
     _check(st, "hca_compress_noalloc")
@@ -326,7 +340,7 @@ def csa_compress_scalar_logits(Ca, Cb, za, zb, ba, bb, m: int = 4, overlap: bool
     _streams(za, (("zb", zb),), ("zb",), overlap)
     _biases(m, 1, overlap, ba=ba, bb=bb)
     out_dtype = Ca.dtype if out_dtype is None else out_dtype
-    out = _out(out, (batch, n // m, c), out_dtype, Ca)
+    out = _out(out, (batch, n // m, c), out_dtype, Ca, stream)
     st = lib().csa_compress_scalar_logits(
         _ptr(Ca), _ptr(Cb) if overlap else None, _ptr(za), _ptr(zb) if overlap else None,
         _dtype_code(Ca.dtype), _ptr(ba), _ptr(bb) if overlap else None, batch, n, c, m,
@@ -342,7 +356,7 @@ def hca_compress_scalar_logits(C, z, b, m: int = 128, out=None, out_dtype=None, 
         raise ValueError("z must be [batch, n] with C's dtype")
     _biases(m, 1, True, b=b)
     out_dtype = C.dtype if out_dtype is None else out_dtype
-    out = _out(out, (batch, n // m, c), out_dtype, C)
+    out = _out(out, (batch, n // m, c), out_dtype, C, stream)
     st = lib().hca_compress_scalar_logits(_ptr(C), _ptr(z), _dtype_code(C.dtype), _ptr(b), batch, n,
                                           c, m, _ptr(out), _dtype_code(out_dtype), _stream(stream))
     _check(st, "hca_compress_scalar_logits")
@@ -365,7 +379,7 @@ def csa_compress_entries(Ca, Cb, Za, Zb, Ba, Bb, seq_start, seq_len, entry, m: i
     _streams(Ca, (("Cb", Cb), ("Za", Za), ("Zb", Zb)), ("Cb", "Zb"), overlap)
     _biases(m, c, overlap, Ba=Ba, Bb=Bb)
     out_dtype = Ca.dtype if out_dtype is None else out_dtype
-    out = _out(out, (num, c), out_dtype, Ca)
+    out = _out(out, (num, c), out_dtype, Ca, stream)
     st = lib().csa_compress_entries(
         _ptr(Ca), _ptr(Cb) if overlap else None, _ptr(Za), _ptr(Zb) if overlap else None,
         _dtype_code(Ca.dtype), _ptr(Ba), _ptr(Bb) if overlap else None, total_rows, c, m,
@@ -383,7 +397,7 @@ def hca_compress_entries(C, Z, B, seq_start, seq_len, entry, m: int = 128, out=N
     _streams(C, (("Z", Z),), (), True)
     _biases(m, c, True, B=B)
     out_dtype = C.dtype if out_dtype is None else out_dtype
-    out = _out(out, (num, c), out_dtype, C)
+    out = _out(out, (num, c), out_dtype, C, stream)
     st = lib().hca_compress_entries(_ptr(C), _ptr(Z), _dtype_code(C.dtype), _ptr(B), total_rows, c,
                                     m, _index(seq_start, num), _index(seq_len, num),
                                     _index(entry, num), num, _ptr(out), _dtype_code(out_dtype),
@@ -392,14 +406,14 @@ def hca_compress_entries(C, Z, B, seq_start, seq_len, entry, m: int = 128, out=N
     return out
 
 
-def _cache_outs(rows, c, r, like, out_nope, out_rope):
+def _cache_outs(rows, c, r, like, out_nope, out_rope, stream):
     # sizes are clamped so that an invalid r reaches the library, which reports it
     torch = _torch()
     cn, rr = max(c - r, 0), max(min(r, c), 0)
     if out_nope is None:
-        out_nope = torch.empty((rows, cn), dtype=torch.uint8, device=like.device)
+        out_nope = _out(None, (rows, cn), torch.uint8, like, stream)
     if out_rope is None:
-        out_rope = torch.empty((rows, rr), dtype=torch.bfloat16, device=like.device)
+        out_rope = _out(None, (rows, rr), torch.bfloat16, like, stream)
     if out_nope.dtype not in (torch.uint8, torch.float8_e4m3fn) or out_nope.numel() != rows * cn:
         raise ValueError("out_nope must hold rows x (c - r) E4M3 bytes")
     if out_rope.dtype != torch.bfloat16 or out_rope.numel() != rows * rr:
@@ -422,7 +436,7 @@ def csa_compress_cache(Ca, Cb, Za, Zb, Ba, Bb, r, inv_freq, pos_stride=4.0, pos_
     _biases(m, c, overlap, Ba=Ba, Bb=Bb)
     _rope_freqs(inv_freq, r, c)
     ne = n // m
-    nope, rope = _cache_outs(batch * ne, c, r, Ca, out_nope, out_rope)
+    nope, rope = _cache_outs(batch * ne, c, r, Ca, out_nope, out_rope, stream)
     st = lib().csa_compress_cache(
         _ptr(Ca), _ptr(Cb) if overlap else None, _ptr(Za), _ptr(Zb) if overlap else None,
         _dtype_code(Ca.dtype), _ptr(Ba), _ptr(Bb) if overlap else None, batch, n, c, m,
@@ -440,7 +454,7 @@ def hca_compress_cache(C, Z, B, r, inv_freq, pos_stride=128.0, pos_offset=63.5, 
     _biases(m, c, True, B=B)
     _rope_freqs(inv_freq, r, c)
     ne = n // m
-    nope, rope = _cache_outs(batch * ne, c, r, C, out_nope, out_rope)
+    nope, rope = _cache_outs(batch * ne, c, r, C, out_nope, out_rope, stream)
     st = lib().hca_compress_cache(_ptr(C), _ptr(Z), _dtype_code(C.dtype), _ptr(B), batch, n, c, m,
                                   *_cache_args(r, inv_freq, pos_stride, pos_offset, fp8_scale, nope,
                                                rope, c), _stream(stream))
@@ -457,7 +471,7 @@ def csa_compress_entries_cache(Ca, Cb, Za, Zb, Ba, Bb, seq_start, seq_len, entry
     _streams(Ca, (("Cb", Cb), ("Za", Za), ("Zb", Zb)), ("Cb", "Zb"), overlap)
     _biases(m, c, overlap, Ba=Ba, Bb=Bb)
     _rope_freqs(inv_freq, r, c)
-    nope, rope = _cache_outs(num, c, r, Ca, out_nope, out_rope)
+    nope, rope = _cache_outs(num, c, r, Ca, out_nope, out_rope, stream)
     st = lib().csa_compress_entries_cache(
         _ptr(Ca), _ptr(Cb) if overlap else None, _ptr(Za), _ptr(Zb) if overlap else None,
         _dtype_code(Ca.dtype), _ptr(Ba), _ptr(Bb) if overlap else None, total_rows, c, m,
@@ -476,7 +490,7 @@ def hca_compress_entries_cache(C, Z, B, seq_start, seq_len, entry, r, inv_freq, 
     _streams(C, (("Z", Z),), (), True)
     _biases(m, c, True, B=B)
     _rope_freqs(inv_freq, r, c)
-    nope, rope = _cache_outs(num, c, r, C, out_nope, out_rope)
+    nope, rope = _cache_outs(num, c, r, C, out_nope, out_rope, stream)
     st = lib().hca_compress_entries_cache(
         _ptr(C), _ptr(Z), _dtype_code(C.dtype), _ptr(B), total_rows, c, m, _index(seq_start, num),
         _index(seq_len, num), _index(entry, num), num,
@@ -497,7 +511,7 @@ def csa_compress_fused_proj(H, W_kva, W_kvb, W_za, W_zb, Ba, Bb, batch: int, n: 
             _need(name, w, d * c, torch.bfloat16)
     _biases(m, c, overlap, Ba=Ba, Bb=Bb)
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
-    out = _out(out, (batch, n // m, c), out_dtype, H)
+    out = _out(out, (batch, n // m, c), out_dtype, H, stream)
     st = lib().csa_compress_fused_proj(
         _ptr(H), _ptr(W_kva), _ptr(W_kvb) if overlap else None, _ptr(W_za),
         _ptr(W_zb) if overlap else None, _ptr(Ba), _ptr(Bb) if overlap else None,
@@ -517,7 +531,7 @@ def hca_compress_fused_proj(H, W_kv, W_z, B, batch: int, n: int, m: int = 128, o
     _need("W_z", W_z, d * c, torch.bfloat16)
     _biases(m, c, True, B=B)
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
-    out = _out(out, (batch, n // m, c), out_dtype, H)
+    out = _out(out, (batch, n // m, c), out_dtype, H, stream)
     st = lib().hca_compress_fused_proj(_ptr(H), _ptr(W_kv), _ptr(W_z), _ptr(B), batch, n, d, c, m,
                                        _ptr(out), _dtype_code(out_dtype), _stream(stream))
     _check(st, "hca_compress_fused_proj")
@@ -538,7 +552,7 @@ def csa_compress_fused_proj_cache(H, W_kva, W_kvb, W_za, W_zb, Ba, Bb, batch: in
     _biases(m, c, True, Ba=Ba, Bb=Bb)
     _rope_freqs(inv_freq, r, c)
     ne = n // m
-    nope, rope = _cache_outs(batch * ne, c, r, H, out_nope, out_rope)
+    nope, rope = _cache_outs(batch * ne, c, r, H, out_nope, out_rope, stream)
     st = lib().csa_compress_fused_proj_cache(
         _ptr(H), _ptr(W_kva), _ptr(W_kvb), _ptr(W_za), _ptr(W_zb), _ptr(Ba), _ptr(Bb), batch, n, d,
         c, m, 1, *_cache_args(r, inv_freq, pos_stride, pos_offset, fp8_scale, nope, rope, c),
@@ -560,7 +574,7 @@ def hca_compress_fused_proj_cache(H, W_kv, W_z, B, batch: int, n: int, r: int, i
     _biases(m, c, True, B=B)
     _rope_freqs(inv_freq, r, c)
     ne = n // m
-    nope, rope = _cache_outs(batch * ne, c, r, H, out_nope, out_rope)
+    nope, rope = _cache_outs(batch * ne, c, r, H, out_nope, out_rope, stream)
     st = lib().hca_compress_fused_proj_cache(
         _ptr(H), _ptr(W_kv), _ptr(W_z), _ptr(B), batch, n, d, c, m,
         *_cache_args(r, inv_freq, pos_stride, pos_offset, fp8_scale, nope, rope, c),
@@ -583,7 +597,7 @@ def csa_compress_fused_proj_scalar(H, W_kva, W_kvb, w_za, w_zb, ba, bb, batch: i
         _need(name, w, d, torch.bfloat16)
     _biases(m, 1, True, ba=ba, bb=bb)
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
-    out = _out(out, (batch, n // m, c), out_dtype, H)
+    out = _out(out, (batch, n // m, c), out_dtype, H, stream)
     st = lib().csa_compress_fused_proj_scalar(
         _ptr(H), _ptr(W_kva), _ptr(W_kvb), _ptr(w_za), _ptr(w_zb), _ptr(ba), _ptr(bb), batch, n,
         d, c, m, 1, _ptr(out), _dtype_code(out_dtype), _stream(stream))
@@ -602,7 +616,7 @@ def hca_compress_fused_proj_scalar(H, W_kv, w_z, b, batch: int, n: int, m: int =
     _need("w_z", w_z, d, torch.bfloat16)
     _biases(m, 1, True, b=b)
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
-    out = _out(out, (batch, n // m, c), out_dtype, H)
+    out = _out(out, (batch, n // m, c), out_dtype, H, stream)
     st = lib().hca_compress_fused_proj_scalar(_ptr(H), _ptr(W_kv), _ptr(w_z), _ptr(b), batch, n, d,
                                               c, m, _ptr(out), _dtype_code(out_dtype),
                                               _stream(stream))
@@ -625,7 +639,8 @@ def lightning_indexer_scores(q, w, K, key_start, n_visible, max_visible: int, sc
     _need("K", K, K.shape[0] * D, torch.bfloat16)
     if scores is None:
         ld = max(4, -(-int(max_visible) // 4) * 4)
-        scores = torch.zeros((T, ld), dtype=torch.float32, device=q.device)
+        scores = _made_on(stream, q, lambda: torch.zeros((T, ld), dtype=torch.float32,
+                                                         device=q.device))
     if scores.dim() != 2 or scores.shape[0] != T or scores.dtype != torch.float32:
         raise ValueError("scores must be fp32 [T, ld]")
     st = lib().lightning_indexer_scores(_ptr(q), _ptr(w), _ptr(K), _index(key_start, T),
@@ -643,25 +658,14 @@ def indexer_topk(scores, n_visible, k: int, max_visible: int, out_idx=None, out_
     torch = _torch()
     T, ld = scores.shape
     _need("scores", scores, T * ld, torch.float32)
-    out_idx = _out(out_idx, (T, k), torch.int32, scores)
+    out_idx = _out(out_idx, (T, k), torch.int32, scores, stream)
     if want_scores:
-        out_score = _out(out_score, (T, k), torch.float32, scores)
+        out_score = _out(out_score, (T, k), torch.float32, scores, stream)
     st = lib().indexer_topk(_ptr(scores), ld, _index(n_visible, T), T, int(max_visible), k,
                             _ptr(out_idx), _ptr(out_score) if want_scores else None,
                             _stream(stream))
     _check(st, "indexer_topk")
     return out_idx, (out_score if want_scores else None)
-
-
-def _made_on(stream, like, make):
-    """make()'s tensor, from the pool of the stream that the kernels are launched on: a block of
-    the current stream's pool may still be written by work queued there, which the launching
-    stream does not wait for."""
-    if stream is None or not like.is_cuda:
-        return make()
-    torch = _torch()
-    with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=like.device)):
-        return make()
 
 
 _ROPE_LAYOUTS = {"interleaved": KVC_ROPE_INTERLEAVED, "half": KVC_ROPE_HALF}
