@@ -88,7 +88,7 @@ constexpr int kStage = kMaxAtoms * kAtom;
 constexpr int kSegs = 8;          // segment records under way
 constexpr int kExps = 4;          // and exponents of Q rows
 // Bounded waits: every wait of a CTA gives up once the CTA has not gone on for kWaitTicks ticks
-// of 2^16 cycles (2 to 3 s).  It goes on when the softmax of a tile ends (microseconds) and when
+// of 2^16 cycles (2 to 3 s).  It goes on when a tile's rows are in place (microseconds) and when
 // the scheduler or a store warp walks over a query, so neither a long query (many tiles before
 // the store warps' next output) nor a padded batch (2^28 queries of which six have rows: 4.2 s
 // in which the other roles have nothing to do; a limit of 2^18 polls gave up there) is taken for
@@ -656,6 +656,7 @@ __device__ __forceinline__ void copy_rows(const Args& a, const Shared& sh) {
     copies_done();
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     sh.arrive(kBKFull + st);
+    if (r == 0) sh.went_on();
     s0 = s1;
     s1 = s2;
   }
@@ -791,7 +792,6 @@ __device__ __forceinline__ void softmax(const Args& a, const Shared& sh) {
       tc_fence_before();
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       sh.arrive(kBPFull + b);
-      if (threadIdx.x == 0) sh.went_on();
     }
     // the sums of the segment before this one have been read
     if (seg > 0 && !sh.wait(kBOFree, (seg - 1) & 1u)) return;
