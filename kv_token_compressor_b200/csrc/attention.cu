@@ -22,7 +22,7 @@
 // exchange cross the SM-to-SM network at 20 bytes a cycle and its latency (about 4000 cycles)
 // sits in every tile's chain: 5300 cycles a tile.
 //
-// What a tile takes: 4250 cycles (chunk of 1024 queries x 1152 rows x 128 heads: 574 us, 530
+// What a tile takes: 4250 cycles (chunk of 1024 queries x 1152 rows x 128 heads: 575 us, 529
 // TFLOP/s).  With every load, conversion, exponential and store taken out 3100 remain, and the
 // hand-overs alone (no MMAs either) take 1000: S of a tile, its softmax, P K and the refill of
 // its place follow one another, two tiles in turn, and S reads Q and K from shared memory at
@@ -41,7 +41,9 @@
 // issues the MMAs, 25 walks the segments (query, row tiles) of its CTA and posts them to the
 // others, 26-27 find each tile's rows, tell the gather and copy the bf16 channels.  A query's
 // tiles are split among CTAs when there are too few queries, and a second kernel joins the
-// parts in a fixed order.
+// parts in a fixed order.  Work is dealt by the longest length a call allows, which the host
+// knows, not by each query's own, which only the device does: queries of one length fill the
+// CTAs alike, ragged ones do not (see plan_of).
 #include <cuda_fp16.h>
 
 #include "kvc_common.cuh"
@@ -1349,6 +1351,9 @@ int least_tiles(int tiles_per_item) {
 // evens that out but costs the parts' way through memory and the join, 20 to 25 us: with 128
 // queries of 1152 rows (256 items, idle for 5 tiles on average) 96 us whole and 102 split, with
 // 700 (9.7 tiles) 422 either way, with 300 (17 tiles) 214 whole and 199 split.
+// Both ways count tiles by the longest length.  Of 64 queries of 1329 to 8320 rows x 128 heads
+// (265 us) the fullest CTA has 113 tiles where the mean is 66.5; of one query of 100000 rows and
+// 73 of 1000 x 128 heads, which go whole, 1563 where the mean is 37.
 constexpr int64_t kIdleTiles = 8;
 
 struct Plan {

@@ -3,15 +3,19 @@
 // and the host-side frequency table scaled for long contexts (kvc_rope_frequencies).
 //
 // Per token the r / 2 angles are shared by all H heads, so a CTA forms each (cos, sin) once in
-// shared memory (angle and reduction in fp64 as for the cache's entries) and applies it to
+// shared memory (angle and reduction in fp64, fp32's rest of the angle put back: within 1.84
+// units in the last place of the angle's own) and applies it to
 // every head it handles; the rotation itself is 3 flops a value, so the kernel is bound by
 // memory traffic (long calls) or by launch and one dependent round trip (short ones).  A unit
 // is one vector of up to 16 bytes (half layout: the vector and its partner r / 2 channels on);
 // every thread has all its kUnits loads in flight before the angles are formed.  Measured:
 // 4096 x 128 heads, r = 64 of c = 512 in place (134 MB, 128 of every 1024 bytes) 29.0 us, 0.71 of
 // the copy bandwidth (1, 2 and 8 units a thread: 36.8, 29.0, 31.4; streaming loads and stores
-// 28.8); 128 x 128 heads 3.2 us and one token 2.4 us, a launch and its round trip; fp32 777 x 24
-// heads of 192 (29 MB, out of place) 6.9 us against 4.4 at the copy bandwidth.
+// 28.8).  What the 128-byte pieces cost in that is not known apart: between events, with cold
+// inputs, the call takes 32.8 us, an elementwise pass of torch in place over as many bytes in one
+// piece 27.4, and over the same pieces 41.8.  128 x 128 heads 3.2 us and one token 2.6 us, a
+// launch and its round trip; fp32 777 x 24 heads of 192 (29 MB, out of place) 7.0 us against 4.4
+// at the copy bandwidth.
 #include <math.h>
 
 #include "kvc_common.cuh"
