@@ -2,7 +2,8 @@
 
 Argument marshalling only: tensors are checked for device, dtype and contiguity, their
 device pointers and the current CUDA stream are passed to libkvc.so, and a non-OK status
-raises :class:`KvcError`.  Every step of the compressor runs in the library's kernels;
+raises :class:`KvcError`.  With ``stream=`` a call runs, and makes the tensors that it
+returns, as under ``torch.cuda.stream``.  Every step of the compressor runs in the library's kernels;
 there is no fallback: if libkvc.so is missing this module raises on first use.
 """
 

@@ -95,3 +95,29 @@ def test_calls_from_several_host_threads():
     for t in threads:
         t.join()
     assert not bad and kvc.device_status() == kvc.KVC_OK
+
+
+def test_captured_on_a_given_stream():
+    """Inside a capture the capturing stream may be named: outputs and workspace then belong to the
+    graph, and replays with new inputs fill the same tensors."""
+    a, b = _args(seed=1), _args(seed=2)
+    pos, f = torch.arange(3, device="cuda"), kvc.rope_frequencies(64)
+
+    def step(x, stream=None):
+        q = kvc.partial_rope(x["q"], pos, f, 64, stream=stream)
+        out, lse = kvc.shared_kv_attention(**{**x, "q": q}, stream=stream)
+        return kvc.partial_rope(out, pos, f, 64, inverse=True, stream=stream), lse
+
+    want = [[t.clone() for t in step(x)] for x in (a, b)]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step(a, torch.cuda.current_stream())
+    junk = [torch.full((1 << 22,), 7.0, device="cuda") for _ in range(4)]
+    for x, w in zip((a, b), want):
+        for name in ("q", "nope", "rope"):
+            a[name].copy_(x[name])
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(s, t) for s, t in zip(got, w))
+    assert all(bool(torch.all(j == 7.0)) for j in junk) and kvc.device_status() == kvc.KVC_OK
